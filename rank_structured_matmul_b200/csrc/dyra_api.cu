@@ -12,7 +12,9 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 
+#include "api_util.h"
 #include "dyra.h"
 #include "dyra_debug.h"
 #include "internal.h"
@@ -109,27 +111,7 @@ struct dyra_plan {
 
 namespace {
 
-size_t elem_size(dyra_dtype_t t) { return t == DYRA_F32 ? 4 : 2; }
-
-bool fail_alloc_for_test() {
-  const char* e = std::getenv("DYRA_TEST_FAIL_ALLOC");
-  return e != nullptr && e[0] == '1';
-}
-
-int dev_alloc(void** p, size_t bytes) {
-  if (fail_alloc_for_test()) return DYRA_ERR_ALLOC;
-  if (cudaMalloc(p, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    *p = nullptr;
-    return DYRA_ERR_ALLOC;
-  }
-  return DYRA_OK;
-}
-
-void dev_free(void*& p) {
-  if (p) cudaFree(p);
-  p = nullptr;
-}
+using namespace dyra;
 
 // Grow a workspace buffer to at least `bytes`.
 int grow(void*& p, size_t& cap, size_t bytes) {
@@ -143,31 +125,12 @@ int grow(void*& p, size_t& cap, size_t bytes) {
   return DYRA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 void drop_graphs(dyra_plan* p) {
   for (auto& g : p->graphs) {
     if (g.exec) cudaGraphExecDestroy(g.exec);
     g = dyra_plan::GraphEntry();
   }
 }
-
-// Run on the plan's device, restoring the caller's device afterwards.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) {
-      ok = false;
-      return;
-    }
-    if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
 
 int ensure_workspace_impl(dyra_plan* p, int64_t B, int64_t T);
 
@@ -597,14 +560,9 @@ int dyra_plan_create_monarch(dyra_plan_t* out, int n, int b1, int b2, int k, dyr
 static int plan_create_impl(dyra_plan_t* out, int d_in, int d_out, int r, int k,
                             dyra_dtype_t dtype) {
 
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return DYRA_ERR_CUDA;
-  }
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return DYRA_ERR_CUDA;
-  if (prop.major != 10 || prop.minor != 0) return DYRA_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  const int drc = current_device_info(&dev);
+  if (drc) return drc;
 
   dyra_plan* p = new (std::nothrow) dyra_plan();
   if (!p) return DYRA_ERR_ALLOC;
@@ -613,13 +571,7 @@ static int plan_create_impl(dyra_plan_t* out, int d_in, int d_out, int r, int k,
   p->r = r;
   p->k = k;
   p->dtype = dtype;
-  p->dev.device = dev;
-  p->dev.sm_count = prop.multiProcessorCount;
-  p->dev.max_smem_optin = static_cast<int>(prop.sharedMemPerBlockOptin);
-  p->dev.smem_per_sm = static_cast<int>(prop.sharedMemPerMultiprocessor);
-  p->dev.smem_reserved = static_cast<int>(prop.reservedSharedMemPerBlock);
-  p->dev.cc_major = prop.major;
-  p->dev.cc_minor = prop.minor;
+  p->dev = dev;
   const char* kv = std::getenv("DYRA_KERNELS");
   p->force_simt = kv != nullptr && std::strcmp(kv, "simt") == 0;
   const char* pv = std::getenv("DYRA_PAIR");

@@ -1,0 +1,66 @@
+// layers.h - interfaces between the ABI of dyra_layers.h (layers_api.cu) and
+// its kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "dyra_layers.h"
+#include "internal.h"
+
+namespace dyra {
+
+// One matrix product with its epilogue, in the form all of the dense layer's
+// products share:
+//   Z[j][m] = sum_k A(m, k) B(j, k) + bias[m],  Out[j][m] = act(Z) + residual[j][m]
+// (m is the output's contiguous index.) An operand is stored K-major (rows of
+// k) or, with a_mn / b_mn, MN-major (rows of m or j).
+//   forward: A = W, B = X;  dX: A = W (MN), B = dZ;  dW: A = X (MN), B = dZ (MN)
+struct LinearGemm {
+  const void* A = nullptr;
+  const void* B = nullptr;
+  bool a_mn = false, b_mn = false;
+  int64_t M = 0, J = 0, K = 0;
+  const void* bias = nullptr;
+  const void* residual = nullptr;
+  int act = DYRA_ACT_NONE;
+  void* Out = nullptr;
+  void* Z = nullptr;
+  int* status = nullptr;
+};
+
+// CUDA-core product (layers_simt.cu): T = float or __nv_bfloat16.
+template <typename T>
+int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
+
+// dZ = dY act'(Z) (skipped for DYRA_ACT_NONE) and its column sums (skipped
+// when dbias is NULL). partial: kColSumChunks x d_out floats; counters:
+// col_sum_blocks(d_out) ints, zero before and after the call.
+constexpr int kColSumChunks = 64;
+int col_sum_blocks(int d_out);
+template <typename T>
+int launch_act_backward(const T* dY, const T* Z, int act, T* dZ, T* dbias, int64_t N, int d_out,
+                        float* partial, int* counters, int* status, const DeviceInfo& dev,
+                        cudaStream_t s);
+
+// ---- experts ----
+
+constexpr int kMoeTokens = 64;  // tokens of one pass over the experts' weights
+
+struct MoeShape {
+  int d, f, experts, top_k, act, renorm;
+};
+
+template <typename T>
+int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float* weights,
+                     int64_t N, int* status, cudaStream_t s);
+
+// CUDA-core experts for N <= kMoeTokens tokens. hidden: N * top_k x f values,
+// part: N * top_k x d floats.
+template <typename T>
+int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
+                            const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
+                            float* part, int* status, cudaStream_t s);
+
+}  // namespace dyra

@@ -1,0 +1,364 @@
+// layers_api.cu - the C ABI declared in include/dyra_layers.h: handles,
+// argument checks, and the choice between the tensor-core kernels (bf16) and
+// the CUDA-core ones (fp32).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdlib>
+#include <cstring>
+#include <new>
+
+#include "api_util.h"
+#include "layers.h"
+
+using namespace dyra;
+
+struct dyra_dense {
+  int d_in = 0, d_out = 0;
+  dyra_dtype_t dtype = DYRA_BF16;
+  DeviceInfo dev;
+  bool simt = false;        // fp32, or DYRA_KERNELS=simt (debugging)
+  float* colsum = nullptr;  // kColSumChunks x d_out partial column sums
+  int* counters = nullptr;  // col_sum_blocks(d_out) arrival counters, zero between calls
+  int* status = nullptr;
+  size_t bytes = 0;
+};
+
+struct dyra_moe {
+  MoeShape m = {};
+  dyra_dtype_t dtype = DYRA_BF16;
+  DeviceInfo dev;
+  bool simt = false;
+  void* hidden = nullptr;  // the hidden values of one group of kMoeTokens tokens
+  float* part = nullptr;   // CUDA cores: its slots' outputs
+  int* status = nullptr;
+  size_t bytes = 0;
+};
+
+namespace {
+
+constexpr int64_t kMaxRows = (static_cast<int64_t>(1) << 31) - 1;
+
+bool simt_requested() {
+  const char* kv = std::getenv("DYRA_KERNELS");
+  return kv != nullptr && std::strcmp(kv, "simt") == 0;
+}
+
+bool known_act(int act) { return act >= DYRA_ACT_NONE && act <= DYRA_ACT_SILU; }
+
+// An allocation of the handle, zeroed, counted in its device bytes.
+template <class T>
+int take(T** p, size_t bytes, size_t* total) {
+  void* v = nullptr;
+  const size_t rounded = (bytes + 255) & ~static_cast<size_t>(255);
+  const int rc = dev_alloc(&v, rounded);
+  if (rc) return rc;
+  *p = static_cast<T*>(v);
+  *total += rounded;
+  // done before any stream can use the handle
+  if (cudaMemset(v, 0, rounded) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+    cudaGetLastError();
+    return DYRA_ERR_CUDA;
+  }
+  return DYRA_OK;
+}
+
+template <class T>
+void give(T*& p) {
+  void* v = p;
+  dev_free(v);
+  p = nullptr;
+}
+
+int read_status(const DeviceInfo& dev, int* status) {
+  DeviceGuard g(dev.device);
+  if (!g.ok || cudaDeviceSynchronize() != cudaSuccess) return DYRA_ERR_CUDA;
+  int st = 0;
+  if (cudaMemcpy(&st, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      cudaMemset(status, 0, sizeof(int)) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess)
+    return DYRA_ERR_CUDA;
+  return st;
+}
+
+int launched(int rc) {
+  if (rc == 0) return DYRA_OK;
+  cudaGetLastError();
+  return DYRA_ERR_CUDA;
+}
+
+int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s) {
+  if (p->dtype == DYRA_F32) return launch_linear_simt<float>(g, p->dev, s);
+  return launch_linear_simt<__nv_bfloat16>(g, p->dev, s);
+}
+
+template <class T>
+int act_backward(const dyra_dense* p, const void* dY, const void* Z, int act, void* dZ,
+                 void* dbias, int64_t N, cudaStream_t s) {
+  return launch_act_backward<T>(static_cast<const T*>(dY), static_cast<const T*>(Z), act,
+                                static_cast<T*>(dZ), static_cast<T*>(dbias), N, p->d_out,
+                                p->colsum, p->counters, p->status, p->dev, s);
+}
+
+void dense_free(dyra_dense* p) {
+  give(p->colsum);
+  give(p->counters);
+  give(p->status);
+  delete p;
+}
+
+void moe_free(dyra_moe* p) {
+  give(p->hidden);
+  give(p->part);
+  give(p->status);
+  delete p;
+}
+
+template <class T>
+int moe_route(const dyra_moe* p, const void* X, const void* Wr, int32_t* ids, float* weights,
+              int64_t N, cudaStream_t s) {
+  return launch_moe_route<T>(p->m, static_cast<const T*>(X), static_cast<const T*>(Wr), ids,
+                             weights, N, p->status, s);
+}
+
+template <class T>
+int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const float* weights,
+                const void* Wgu, const void* Wd, const void* residual, void* Y, int n,
+                cudaStream_t s) {
+  return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
+                                    static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
+                                    static_cast<const T*>(residual), static_cast<T*>(Y), n,
+                                    static_cast<T*>(p->hidden), p->part, p->status, s);
+}
+
+// The shared checks of the calls on N tokens: DYRA_OK to go on.
+int moe_check(const dyra_moe* p, int64_t N) {
+  if (p == nullptr || N < 0 || N > kMaxRows) return DYRA_ERR_INVALID_ARG;
+  return DYRA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dyra_dense_create(dyra_dense_t* out, int d_in, int d_out, dyra_dtype_t dtype) {
+  if (out == nullptr) return DYRA_ERR_INVALID_ARG;
+  if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_ERR_INVALID_ARG;
+  if (d_in < 1 || d_out < 1) return DYRA_ERR_INVALID_ARG;
+  if (dtype == DYRA_BF16 && (d_in % 8 || d_out % 8)) return DYRA_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  int rc = current_device_info(&dev);
+  if (rc) return rc;
+  dyra_dense* p = new (std::nothrow) dyra_dense();
+  if (!p) return DYRA_ERR_ALLOC;
+  p->d_in = d_in;
+  p->d_out = d_out;
+  p->dtype = dtype;
+  p->dev = dev;
+  p->simt = dtype == DYRA_F32 || simt_requested();
+  if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
+      (rc = take(&p->colsum, sizeof(float) * kColSumChunks * d_out, &p->bytes)) ||
+      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes))) {
+    dense_free(p);
+    return rc;
+  }
+  *out = p;
+  return DYRA_OK;
+}
+
+int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void* bias,
+                       const void* residual, int act, void* Y, void* Z, int64_t N,
+                       dyra_stream_t stream) {
+  if (p == nullptr || N < 0 || N > kMaxRows || !known_act(act)) return DYRA_ERR_INVALID_ARG;
+  if (N == 0) return DYRA_OK;
+  if (X == nullptr || W == nullptr || Y == nullptr) return DYRA_ERR_INVALID_ARG;
+  for (const void* q : {X, W, bias, residual, static_cast<const void*>(Y),
+                        static_cast<const void*>(Z)})
+    if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  DeviceGuard dg(p->dev.device);
+  if (!dg.ok) return DYRA_ERR_CUDA;
+  LinearGemm g;
+  g.A = W;
+  g.B = X;
+  g.M = p->d_out;
+  g.J = N;
+  g.K = p->d_in;
+  g.bias = bias;
+  g.residual = residual;
+  g.act = act;
+  g.Out = Y;
+  g.Z = Z;
+  g.status = p->status;
+  return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const void* W,
+                        const void* Z, int act, void* dZ, void* dX, void* dW, void* dbias,
+                        int64_t N, dyra_stream_t stream) {
+  if (p == nullptr || N < 0 || N > kMaxRows || !known_act(act)) return DYRA_ERR_INVALID_ARG;
+  const bool has_act = act != DYRA_ACT_NONE;
+  if (N > 0 && (dY == nullptr || (dW != nullptr && X == nullptr) ||
+                (dX != nullptr && W == nullptr) || (has_act && (Z == nullptr || dZ == nullptr))))
+    return DYRA_ERR_INVALID_ARG;
+  for (const void* q : {dY, X, W, Z, static_cast<const void*>(dZ), static_cast<const void*>(dX),
+                        static_cast<const void*>(dW), static_cast<const void*>(dbias)})
+    if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  DeviceGuard dg(p->dev.device);
+  if (!dg.ok) return DYRA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t es = elem_size(p->dtype);
+  if (N == 0) {
+    if ((dW && cudaMemsetAsync(dW, 0, es * p->d_out * p->d_in, s) != cudaSuccess) ||
+        (dbias && cudaMemsetAsync(dbias, 0, es * p->d_out, s) != cudaSuccess))
+      return launched(-1);
+    return DYRA_OK;
+  }
+  if (has_act || dbias) {
+    const int rc = p->dtype == DYRA_F32
+                       ? act_backward<float>(p, dY, Z, act, dZ, dbias, N, s)
+                       : act_backward<__nv_bfloat16>(p, dY, Z, act, dZ, dbias, N, s);
+    if (rc) return launched(rc);
+  }
+  LinearGemm g;
+  g.status = p->status;
+  g.B = has_act ? dZ : dY;
+  g.M = p->d_in;
+  if (dX) {
+    g.A = W;
+    g.a_mn = true;
+    g.J = N;
+    g.K = p->d_out;
+    g.Out = dX;
+    const int rc = linear(p, g, s);
+    if (rc) return launched(rc);
+  }
+  if (dW) {
+    g.A = X;
+    g.a_mn = g.b_mn = true;
+    g.J = p->d_out;
+    g.K = N;
+    g.Out = dW;
+    const int rc = linear(p, g, s);
+    if (rc) return launched(rc);
+  }
+  return DYRA_OK;
+}
+
+int dyra_dense_status(dyra_dense_t p) {
+  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status);
+}
+
+size_t dyra_dense_device_bytes(dyra_dense_t p) { return p == nullptr ? 0 : p->bytes; }
+
+int dyra_dense_destroy(dyra_dense_t p) {
+  if (p == nullptr) return DYRA_OK;
+  DeviceGuard g(p->dev.device);
+  cudaDeviceSynchronize();
+  dense_free(p);
+  return DYRA_OK;
+}
+
+int dyra_moe_create(dyra_moe_t* out, int d_model, int d_ff, int experts, int top_k, int act,
+                    int renorm, dyra_dtype_t dtype) {
+  if (out == nullptr) return DYRA_ERR_INVALID_ARG;
+  if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_ERR_INVALID_ARG;
+  if (d_model < 1 || d_ff < 1 || d_ff > (1 << 29) || experts < 1 ||
+      experts > DYRA_MOE_MAX_EXPERTS || top_k < 1 || top_k > DYRA_MOE_MAX_TOP_K ||
+      top_k > experts || !known_act(act) || (renorm != 0 && renorm != 1))
+    return DYRA_ERR_INVALID_ARG;
+  if (dtype == DYRA_BF16 && (d_model % 8 || d_ff % 8)) return DYRA_ERR_ALIGNMENT;
+  DeviceInfo dev;
+  int rc = current_device_info(&dev);
+  if (rc) return rc;
+  dyra_moe* p = new (std::nothrow) dyra_moe();
+  if (!p) return DYRA_ERR_ALLOC;
+  p->m = MoeShape{d_model, d_ff, experts, top_k, act, renorm};
+  p->dtype = dtype;
+  p->dev = dev;
+  p->simt = dtype == DYRA_F32 || simt_requested();
+  const size_t slots = static_cast<size_t>(kMoeTokens) * top_k;
+  if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
+      (rc = take(&p->hidden, slots * d_ff * elem_size(dtype), &p->bytes)) ||
+      (rc = take(&p->part, slots * d_model * sizeof(float), &p->bytes))) {
+    moe_free(p);
+    return rc;
+  }
+  *out = p;
+  return DYRA_OK;
+}
+
+int dyra_moe_route(dyra_moe_t p, const void* X, const void* Wr, int32_t* ids, float* weights,
+                   int64_t N, dyra_stream_t stream) {
+  const int rc = moe_check(p, N);
+  if (rc || N == 0) return rc;
+  if (X == nullptr || Wr == nullptr || ids == nullptr || weights == nullptr)
+    return DYRA_ERR_INVALID_ARG;
+  if (!aligned16(X) || !aligned16(Wr) || !aligned16(ids) || !aligned16(weights))
+    return DYRA_ERR_ALIGNMENT;
+  DeviceGuard g(p->dev.device);
+  if (!g.ok) return DYRA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launched(p->dtype == DYRA_F32
+                      ? moe_route<float>(p, X, Wr, ids, weights, N, s)
+                      : moe_route<__nv_bfloat16>(p, X, Wr, ids, weights, N, s));
+}
+
+int dyra_moe_experts(dyra_moe_t p, const void* X, const int32_t* ids, const float* weights,
+                     const void* Wgu, const void* Wd, const void* residual, void* Y, int64_t N,
+                     dyra_stream_t stream) {
+  int rc = moe_check(p, N);
+  if (rc || N == 0) return rc;
+  if (X == nullptr || ids == nullptr || weights == nullptr || Wgu == nullptr || Wd == nullptr ||
+      Y == nullptr)
+    return DYRA_ERR_INVALID_ARG;
+  for (const void* q : {X, static_cast<const void*>(ids), static_cast<const void*>(weights), Wgu,
+                        Wd, residual, static_cast<const void*>(Y)})
+    if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  DeviceGuard g(p->dev.device);
+  if (!g.ok) return DYRA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const size_t row = elem_size(p->dtype) * p->m.d;
+  for (int64_t n0 = 0; n0 < N && rc == 0; n0 += kMoeTokens) {
+    const int n = static_cast<int>(std::min<int64_t>(kMoeTokens, N - n0));
+    const void* x = static_cast<const char*>(X) + n0 * row;
+    const void* r = residual ? static_cast<const char*>(residual) + n0 * row : nullptr;
+    void* y = static_cast<char*>(Y) + n0 * row;
+    rc = p->dtype == DYRA_F32
+             ? moe_experts<float>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k, Wgu, Wd,
+                                  r, y, n, s)
+             : moe_experts<__nv_bfloat16>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k,
+                                          Wgu, Wd, r, y, n, s);
+  }
+  return launched(rc);
+}
+
+int dyra_moe_forward(dyra_moe_t p, const void* X, const void* Wr, const void* Wgu, const void* Wd,
+                     const void* residual, void* Y, int32_t* ids, float* weights, int64_t N,
+                     dyra_stream_t stream) {
+  int rc = moe_check(p, N);
+  if (rc || N == 0) return rc;
+  // the experts' arguments are refused before the router is enqueued
+  if (Wgu == nullptr || Wd == nullptr || Y == nullptr) return DYRA_ERR_INVALID_ARG;
+  if (!aligned16(Wgu) || !aligned16(Wd) || !aligned16(residual) || !aligned16(Y))
+    return DYRA_ERR_ALIGNMENT;
+  rc = dyra_moe_route(p, X, Wr, ids, weights, N, stream);
+  if (rc) return rc;
+  return dyra_moe_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, stream);
+}
+
+int dyra_moe_status(dyra_moe_t p) {
+  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status);
+}
+
+size_t dyra_moe_device_bytes(dyra_moe_t p) { return p == nullptr ? 0 : p->bytes; }
+
+int dyra_moe_destroy(dyra_moe_t p) {
+  if (p == nullptr) return DYRA_OK;
+  DeviceGuard g(p->dev.device);
+  cudaDeviceSynchronize();
+  moe_free(p);
+  return DYRA_OK;
+}
+
+}  // extern "C"

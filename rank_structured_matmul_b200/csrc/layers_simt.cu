@@ -1,0 +1,443 @@
+// layers_simt.cu - CUDA-core kernels of the dense and expert layers: the fp32
+// products (fp32 accuracy needs plain FFMA; TF32 would lose ~1e-3), the
+// activation's backward with its column sums, and the router.
+#include <algorithm>
+
+#include "layers.h"
+#include "layers_math.cuh"
+#include "sm100.cuh"
+
+namespace dyra {
+
+namespace {
+
+// ------------------------------------------------------------ dense gemm ----
+// Out[j][m] tile of 64 G x 64 G, 256 threads with 4 G x 4 G values each, k in
+// steps of 16 through two shared-memory buffers: the loads of step s + 1 are in
+// flight while step s is multiplied. Loads are element-wise (rows of odd
+// length have no common alignment) with consecutive threads on the stored
+// matrix's contiguous index.
+constexpr int kSimtBk = 16;
+
+template <typename T, bool AMN, bool BMN, int G>
+__global__ void __launch_bounds__(256)
+    linear_simt_kernel(LinearGemm g, int64_t m_tiles) {
+  constexpr int BT = 64 * G;
+  constexpr int PER = BT * kSimtBk / 256;
+  __shared__ __align__(16) float As[2][kSimtBk][BT + 4];
+  __shared__ __align__(16) float Bs[2][kSimtBk][BT + 4];
+  const T* __restrict__ A = static_cast<const T*>(g.A);
+  const T* __restrict__ B = static_cast<const T*>(g.B);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int64_t jt = blockIdx.x / m_tiles;
+  const int64_t m0 = (blockIdx.x - jt * m_tiles) * BT, j0 = jt * BT;
+  float ra[PER], rb[PER];
+  auto fetch = [&](int64_t k0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int idx = threadIdx.x + 256 * i;
+      const int ka = AMN ? idx / BT : idx % kSimtBk, ma = AMN ? idx % BT : idx / kSimtBk;
+      const int kb = BMN ? idx / BT : idx % kSimtBk, jb = BMN ? idx % BT : idx / kSimtBk;
+      const int64_t gm = m0 + ma, gka = k0 + ka, gj = j0 + jb, gkb = k0 + kb;
+      ra[i] = gm < g.M && gka < g.K ? load_f(A[AMN ? gka * g.M + gm : gm * g.K + gka]) : 0.f;
+      rb[i] = gj < g.J && gkb < g.K ? load_f(B[BMN ? gkb * g.J + gj : gj * g.K + gkb]) : 0.f;
+    }
+  };
+  auto stash = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int idx = threadIdx.x + 256 * i;
+      As[buf][AMN ? idx / BT : idx % kSimtBk][AMN ? idx % BT : idx / kSimtBk] = ra[i];
+      Bs[buf][BMN ? idx / BT : idx % kSimtBk][BMN ? idx % BT : idx / kSimtBk] = rb[i];
+    }
+  };
+  float acc[4 * G][4 * G] = {};
+  fetch(0);
+  stash(0);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k0 = 0; k0 < g.K; k0 += kSimtBk, buf ^= 1) {
+    const bool more = k0 + kSimtBk < g.K;
+    if (more) fetch(k0 + kSimtBk);
+#pragma unroll
+    for (int k = 0; k < kSimtBk; ++k) {
+      float a[4 * G], b[4 * G];
+#pragma unroll
+      for (int q = 0; q < G; ++q) {
+        const float4 av = *reinterpret_cast<const float4*>(&As[buf][k][64 * q + 4 * tx]);
+        const float4 bv = *reinterpret_cast<const float4*>(&Bs[buf][k][64 * q + 4 * ty]);
+        a[4 * q] = av.x, a[4 * q + 1] = av.y, a[4 * q + 2] = av.z, a[4 * q + 3] = av.w;
+        b[4 * q] = bv.x, b[4 * q + 1] = bv.y, b[4 * q + 2] = bv.z, b[4 * q + 3] = bv.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * G; ++j)
+#pragma unroll
+        for (int m = 0; m < 4 * G; ++m) acc[j][m] = fmaf(b[j], a[m], acc[j][m]);
+    }
+    if (more) stash(buf ^ 1);
+    __syncthreads();
+  }
+  const T* __restrict__ bias = static_cast<const T*>(g.bias);
+  const T* residual = static_cast<const T*>(g.residual);  // may be Out: no __restrict__
+  T* Out = static_cast<T*>(g.Out);
+  T* Z = static_cast<T*>(g.Z);
+  with_act(g.act, [&](auto tag) {
+    constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+    for (int j = 0; j < 4 * G; ++j) {
+      const int64_t gj = j0 + 64 * (j / 4) + 4 * ty + (j & 3);
+      if (gj >= g.J) continue;
+#pragma unroll
+      for (int m = 0; m < 4 * G; ++m) {
+        const int64_t gm = m0 + 64 * (m / 4) + 4 * tx + (m & 3);
+        if (gm >= g.M) continue;
+        const size_t at = static_cast<size_t>(gj) * g.M + gm;
+        if (!sm100::in_bounds(g.status, at, 1, static_cast<size_t>(g.J) * g.M)) continue;
+        float z = acc[j][m];
+        if (bias) z += load_f(bias[gm]);
+        if (Z) Z[at] = store_f<T>(z);
+        float y = act_f<ACT>(z);
+        if (residual) y += load_f(residual[at]);
+        Out[at] = store_f<T>(y);
+      }
+    }
+  });
+}
+
+template <typename T, int G>
+int launch_linear_simt_g(const LinearGemm& g, cudaStream_t s) {
+  constexpr int BT = 64 * G;
+  const int64_t mt = (g.M + BT - 1) / BT, jt = (g.J + BT - 1) / BT;
+  if (mt * jt > 0x7fffffffll) return -1;
+  const dim3 grid(static_cast<unsigned>(mt * jt));
+  if (g.a_mn && g.b_mn)
+    linear_simt_kernel<T, true, true, G><<<grid, 256, 0, s>>>(g, mt);
+  else if (g.a_mn)
+    linear_simt_kernel<T, true, false, G><<<grid, 256, 0, s>>>(g, mt);
+  else
+    linear_simt_kernel<T, false, false, G><<<grid, 256, 0, s>>>(g, mt);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+// ---------------------------------------------------- activation backward ----
+// dZ = dY act'(Z) and the column sums of dZ, in one pass over dY and Z. A block
+// takes 32 V columns (V values per thread: one 16-byte piece where rows are
+// aligned, else single values) and every 8 x chunks-th row; the sums of its 8
+// row lanes meet in shared memory, the chunks' sums in `partial`, and the last
+// block of a column group to arrive adds the chunks in order and rounds once.
+template <typename T, int V>
+struct Piece {
+  T v[V];
+};
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(256)
+    act_backward_kernel(const T* dY, const T* Z, T* dZ, T* __restrict__ dbias, int64_t N, int d_out,
+                        float* __restrict__ partial, int* counters, int* status) {
+  struct alignas(sizeof(T) * V) P {
+    T v[V];
+  };
+  const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int col = (blockIdx.x * 32 + lane) * V;
+  float sum[V] = {};
+  if (col < d_out) {
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + rl; r < N;
+         r += static_cast<int64_t>(gridDim.y) * 8) {
+      const size_t at = static_cast<size_t>(r) * d_out + col;
+      if (!sm100::in_bounds(status, at, V, static_cast<size_t>(N) * d_out)) continue;
+      const P g = *reinterpret_cast<const P*>(dY + at);
+      P out;
+      if (ACT != DYRA_ACT_NONE) {
+        const P z = *reinterpret_cast<const P*>(Z + at);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          // a zero slope of the ReLU is a zero gradient, whatever dY holds
+          const float d = ACT == DYRA_ACT_RELU
+                              ? (load_f(z.v[i]) > 0.f ? load_f(g.v[i]) : 0.f)
+                              : load_f(g.v[i]) * act_grad_f<ACT>(load_f(z.v[i]));
+          sum[i] += d;
+          out.v[i] = store_f<T>(d);
+        }
+        *reinterpret_cast<P*>(dZ + at) = out;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += load_f(g.v[i]);
+      }
+    }
+  }
+  if (dbias == nullptr) return;
+  __shared__ float red[8][32 * V + 1];
+  __shared__ int last;
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[rl][lane * V + i] = sum[i];
+  __syncthreads();
+  const int c0 = blockIdx.x * 32 * V;
+  for (int c = threadIdx.x; c < 32 * V; c += 256) {
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += red[q][c];
+    if (c0 + c < d_out) partial[static_cast<size_t>(blockIdx.y) * d_out + c0 + c] = t;
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(&counters[blockIdx.x], 1) == static_cast<int>(gridDim.y) - 1;
+    if (last) counters[blockIdx.x] = 0;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int c = threadIdx.x; c < 32 * V; c += 256) {
+    if (c0 + c >= d_out) continue;
+    float t = 0.f;
+    for (int q = 0; q < static_cast<int>(gridDim.y); ++q)
+      t += __ldcg(partial + static_cast<size_t>(q) * d_out + c0 + c);
+    dbias[c0 + c] = store_f<T>(t);
+  }
+}
+
+template <typename T, int V>
+int launch_act_backward_v(const T* dY, const T* Z, int act, T* dZ, T* dbias, int64_t N, int d_out,
+                          float* partial, int* counters, int* status, const DeviceInfo& dev,
+                          cudaStream_t s) {
+  const int cols = (d_out + 32 * V - 1) / (32 * V);
+  // about four blocks of 256 threads per SM, each with at least one row per lane
+  const int64_t want = std::max<int64_t>(1, 4 * dev.sm_count / cols);
+  const int chunks = static_cast<int>(
+      std::min<int64_t>({want, std::max<int64_t>(1, (N + 7) / 8), kColSumChunks}));
+  with_act(act, [&](auto tag) {
+    act_backward_kernel<T, V, decltype(tag)::value><<<dim3(cols, chunks), 256, 0, s>>>(
+        dY, Z, dZ, dbias, N, d_out, partial, counters, status);
+  });
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+// ----------------------------------------------------------------- router ----
+// One block per token: each warp takes every 8th expert, its lanes eight
+// consecutive products each (summed in fp32, then added in fp64: the choice
+// of experts is discrete, so logits near the border of the top k must not
+// depend on the order of a long fp32 sum). The first warp then picks the
+// largest logit top_k times.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    moe_route_kernel(MoeShape m, const T* __restrict__ X, const T* __restrict__ Wr,
+                     int* __restrict__ ids, float* __restrict__ weights) {
+  __shared__ double logit[DYRA_MOE_MAX_EXPERTS];
+  const int64_t n = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = X + n * m.d;
+  for (int e = warp; e < m.experts; e += 8) {
+    const T* w = Wr + static_cast<size_t>(e) * m.d;
+    double acc = 0.0;
+    for (int i = lane * 8; i < m.d; i += 256) {
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (i + q < m.d) t = fmaf(load_f(x[i + q]), load_f(w[i + q]), t);
+      acc += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane == 0) logit[e] = acc;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // expert 32 i + lane is this lane's i-th; a set bit of taken marks a chosen one
+  unsigned taken = 0;
+  double top = 0.0;
+  float mine = 0.f, sum = 0.f;
+  int my_id = 0;
+  const double ninf = -INFINITY;
+  for (int k = 0; k < m.top_k; ++k) {
+    double best = 0.0;
+    int at = 0x7fffffff;
+    for (int e = lane, i = 0; e < m.experts; e += 32, ++i) {
+      if (taken >> i & 1) continue;
+      const double v = isnan(logit[e]) ? ninf : logit[e];
+      if (at == 0x7fffffff || v > best) best = v, at = e;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+      if (oa != 0x7fffffff && (at == 0x7fffffff || ob > best || (ob == best && oa < at)))
+        best = ob, at = oa;
+    }
+    if ((at & 31) == lane) taken |= 1u << (at >> 5);
+    if (k == 0) top = logit[at];
+    const float p = expf(static_cast<float>(logit[at] - top));
+    sum += p;
+    if (lane == k) mine = p, my_id = at;
+  }
+  if (!m.renorm) {
+    sum = 0.f;
+    for (int e = lane; e < m.experts; e += 32) sum += expf(static_cast<float>(logit[e] - top));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  if (lane < m.top_k) {
+    ids[n * m.top_k + lane] = my_id;
+    weights[n * m.top_k + lane] = mine / sum;
+  }
+}
+
+// ---------------------------------------------------------------- experts ----
+// CUDA-core experts: a warp per output row of one expert, over the slots
+// (token, k) that name it, eight at a time: each weight is read once per eight
+// slots. STAGE 0: hidden[slot] = act(g) u over rows f; STAGE 1: part[slot] over
+// rows d. The slots of the block's expert are listed in order first.
+template <typename T, int STAGE>
+__global__ void __launch_bounds__(256)
+    moe_expert_kernel(MoeShape m, const T* __restrict__ In, const int* __restrict__ ids,
+                      const T* __restrict__ W, T* __restrict__ hidden, float* __restrict__ part,
+                      int N, int act, int* status) {
+  __shared__ int list[kMoeTokens * DYRA_MOE_MAX_TOP_K];
+  __shared__ int count;
+  const int e = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slots = N * m.top_k;
+  if (warp == 0) {
+    int c = 0;
+    for (int i0 = 0; i0 < slots; i0 += 32) {
+      const int i = i0 + lane;
+      const bool hit = i < slots && ids[i] == e;
+      const unsigned b = __ballot_sync(0xffffffffu, hit);
+      if (hit) list[c + __popc(b & ((1u << lane) - 1))] = i;
+      c += __popc(b);
+    }
+    if (lane == 0) count = c;
+  }
+  __syncthreads();
+  const int nsl = count;
+  if (nsl == 0) return;
+  const int rows = STAGE == 0 ? m.f : m.d, K = STAGE == 0 ? m.d : m.f;
+  const size_t wrows = STAGE == 0 ? 2 * static_cast<size_t>(m.f) : m.d;
+  const T* We = W + wrows * e * K;
+  const int row = blockIdx.x * 8 + warp;
+  if (row >= rows) return;
+  const T* w0 = We + static_cast<size_t>(row) * K;
+  const T* w1 = STAGE == 0 ? We + static_cast<size_t>(m.f + row) * K : w0;
+  for (int s0 = 0; s0 < nsl; s0 += 8) {
+    float a0[8] = {}, a1[8] = {};
+    const T* x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int slot = list[min(s0 + q, nsl - 1)];
+      x[q] = In + static_cast<size_t>(STAGE == 0 ? slot / m.top_k : slot) * K;
+    }
+    for (int i = lane; i < K; i += 32) {
+      const float v0 = load_f(w0[i]), v1 = STAGE == 0 ? load_f(w1[i]) : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float xv = load_f(x[q][i]);
+        a0[q] = fmaf(v0, xv, a0[q]);
+        if (STAGE == 0) a1[q] = fmaf(v1, xv, a1[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        a0[q] += __shfl_xor_sync(0xffffffffu, a0[q], o);
+        if (STAGE == 0) a1[q] += __shfl_xor_sync(0xffffffffu, a1[q], o);
+      }
+      if (lane == 0 && s0 + q < nsl) {
+        const size_t at = static_cast<size_t>(list[s0 + q]) * rows + row;
+        if (!sm100::in_bounds(status, at, 1, static_cast<size_t>(slots) * rows)) continue;
+        if (STAGE == 0)
+          with_act(act, [&](auto tag) {
+            hidden[at] = store_f<T>(act_f<decltype(tag)::value>(a0[q]) * a1[q]);
+          });
+        else
+          part[at] = a0[q];
+      }
+    }
+  }
+}
+
+// Y[n] = sum over k, in order, of weights[n][k] part[n][k] + residual[n]
+template <typename T>
+__global__ void __launch_bounds__(256)
+    moe_combine_kernel(MoeShape m, const int* __restrict__ ids, const float* __restrict__ weights,
+                       const float* __restrict__ part, const T* residual, T* Y, int N,
+                       int* status) {
+  const int n = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= m.d) return;
+  float acc = 0.f;
+  for (int k = 0; k < m.top_k; ++k) {
+    const int slot = n * m.top_k + k, e = ids[slot];
+    if (e >= 0 && e < m.experts)
+      acc = fmaf(weights[slot], part[static_cast<size_t>(slot) * m.d + i], acc);
+  }
+  const size_t at = static_cast<size_t>(n) * m.d + i;
+  if (!sm100::in_bounds(status, at, 1, static_cast<size_t>(N) * m.d)) return;
+  if (residual) acc += load_f(residual[at]);
+  Y[at] = store_f<T>(acc);
+}
+
+}  // namespace
+
+// 128 x 128 tiles once they fill the SMs; below that 64 x 64 tiles spread the
+// work over more of them.
+template <typename T>
+int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t big = ((g.M + 127) / 128) * ((g.J + 127) / 128);
+  return big >= dev.sm_count ? launch_linear_simt_g<T, 2>(g, s) : launch_linear_simt_g<T, 1>(g, s);
+}
+template int launch_linear_simt<float>(const LinearGemm&, const DeviceInfo&, cudaStream_t);
+template int launch_linear_simt<__nv_bfloat16>(const LinearGemm&, const DeviceInfo&, cudaStream_t);
+
+int col_sum_blocks(int d_out) { return (d_out + 31) / 32; }
+
+template <typename T>
+int launch_act_backward(const T* dY, const T* Z, int act, T* dZ, T* dbias, int64_t N, int d_out,
+                        float* partial, int* counters, int* status, const DeviceInfo& dev,
+                        cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  if (d_out % V == 0)
+    return launch_act_backward_v<T, V>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
+                                       dev, s);
+  return launch_act_backward_v<T, 1>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
+                                     dev, s);
+}
+template int launch_act_backward<float>(const float*, const float*, int, float*, float*, int64_t,
+                                        int, float*, int*, int*, const DeviceInfo&, cudaStream_t);
+template int launch_act_backward<__nv_bfloat16>(const __nv_bfloat16*, const __nv_bfloat16*, int,
+                                                __nv_bfloat16*, __nv_bfloat16*, int64_t, int,
+                                                float*, int*, int*, const DeviceInfo&,
+                                                cudaStream_t);
+
+template <typename T>
+int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float* weights,
+                     int64_t N, int* status, cudaStream_t s) {
+  (void)status;
+  moe_route_kernel<T><<<static_cast<unsigned>(N), 256, 0, s>>>(m, X, Wr, ids, weights);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+template int launch_moe_route<float>(const MoeShape&, const float*, const float*, int*, float*,
+                                     int64_t, int*, cudaStream_t);
+template int launch_moe_route<__nv_bfloat16>(const MoeShape&, const __nv_bfloat16*,
+                                             const __nv_bfloat16*, int*, float*, int64_t, int*,
+                                             cudaStream_t);
+
+template <typename T>
+int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
+                            const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
+                            float* part, int* status, cudaStream_t s) {
+  moe_expert_kernel<T, 0><<<dim3((m.f + 7) / 8, m.experts), 256, 0, s>>>(
+      m, X, ids, Wgu, hidden, nullptr, N, m.act, status);
+  moe_expert_kernel<T, 1><<<dim3((m.d + 7) / 8, m.experts), 256, 0, s>>>(
+      m, hidden, ids, Wd, nullptr, part, N, m.act, status);
+  moe_combine_kernel<T><<<dim3((m.d + 255) / 256, N), 256, 0, s>>>(m, ids, weights, part, residual,
+                                                                   Y, N, status);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+template int launch_moe_experts_simt<float>(const MoeShape&, const float*, const int*,
+                                            const float*, const float*, const float*, const float*,
+                                            float*, int, float*, float*, int*, cudaStream_t);
+template int launch_moe_experts_simt<__nv_bfloat16>(
+    const MoeShape&, const __nv_bfloat16*, const int*, const float*, const __nv_bfloat16*,
+    const __nv_bfloat16*, const __nv_bfloat16*, __nv_bfloat16*, int, __nv_bfloat16*, float*, int*,
+    cudaStream_t);
+
+}  // namespace dyra

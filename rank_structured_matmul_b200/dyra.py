@@ -35,7 +35,7 @@ DYRA_STATUS_NONPOSITIVE_PIVOT = 1
 DYRA_STATUS_WAIT_TIMEOUT = 2
 DYRA_STATUS_BOUNDS = 4
 
-# name -> (restype, argtypes), mirroring include/dyra.h
+# name -> (restype, argtypes), mirroring include/*.h
 _vp, _i, _i64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "dyra_plan_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i]),
@@ -56,6 +56,19 @@ SIGNATURES = {
     "dyra_plan_destroy": (_i, [_vp]),
     "dyra_error_string": (ctypes.c_char_p, [_i]),
     "dyra_plan_device_bytes": (ctypes.c_size_t, [_vp]),
+    "dyra_dense_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i]),
+    "dyra_dense_forward": (_i, [_vp] * 5 + [_i, _vp, _vp, _i64, _vp]),
+    "dyra_dense_backward": (_i, [_vp] * 5 + [_i, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "dyra_dense_status": (_i, [_vp]),
+    "dyra_dense_device_bytes": (ctypes.c_size_t, [_vp]),
+    "dyra_dense_destroy": (_i, [_vp]),
+    "dyra_moe_create": (_i, [ctypes.POINTER(_vp), _i, _i, _i, _i, _i, _i, _i]),
+    "dyra_moe_route": (_i, [_vp] * 5 + [_i64, _vp]),
+    "dyra_moe_experts": (_i, [_vp] * 8 + [_i64, _vp]),
+    "dyra_moe_forward": (_i, [_vp] * 9 + [_i64, _vp]),
+    "dyra_moe_status": (_i, [_vp]),
+    "dyra_moe_device_bytes": (ctypes.c_size_t, [_vp]),
+    "dyra_moe_destroy": (_i, [_vp]),
     "dyra_debug_buffer": (_i, [_vp, _i, ctypes.POINTER(_vp), ctypes.POINTER(ctypes.c_size_t)]),
     "dyra_debug_copy": (_i, [_vp, _i, _vp, ctypes.c_size_t]),
     "dyra_debug_gram_split": (_i, [_vp, _i64, _i64, ctypes.POINTER(_i), ctypes.POINTER(_i)]),

@@ -1,0 +1,296 @@
+"""Exact layers beside the approximated one (include/dyra_layers.h).
+
+DenseLinear: a dense linear layer with bias, activation and residual in its
+epilogue, and its gradients. MoeLayer: a mixture-of-experts layer for a few
+tokens. As in dyra.py this marshals arguments only; every step runs in
+libdyra.so's CUDA kernels and there is no fallback.
+
+Weights are arguments of each call. Tensors are contiguous CUDA tensors of the
+layer's type on the layer's device (the current device when it was made); a
+call runs on `stream` (default: that device's current stream), where its
+results are allocated too.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional
+
+from .dyra import DYRA_BF16, DYRA_F32, _check, _ptr, lib
+
+DYRA_ACT_NONE = 0
+DYRA_ACT_RELU = 1
+DYRA_ACT_GELU = 2
+DYRA_ACT_GELU_TANH = 3
+DYRA_ACT_SILU = 4
+ACTIVATIONS = {"none": DYRA_ACT_NONE, "relu": DYRA_ACT_RELU, "gelu": DYRA_ACT_GELU,
+               "gelu_tanh": DYRA_ACT_GELU_TANH, "silu": DYRA_ACT_SILU}
+
+DYRA_MOE_MAX_TOP_K = 16
+DYRA_MOE_MAX_EXPERTS = 512
+
+
+# ---- raw C-ABI wrappers (same names; ints or tensors for pointers) ----
+
+def dyra_dense_create(d_in: int, d_out: int, dtype: int) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().dyra_dense_create(ctypes.byref(h), d_in, d_out, dtype), "dyra_dense_create")
+    return h.value
+
+
+def dyra_dense_forward(p: int, X, W, bias, residual, act: int, Y, Z, N: int, stream) -> None:
+    _check(lib().dyra_dense_forward(p, _ptr(X), _ptr(W), _ptr(bias), _ptr(residual), act, _ptr(Y),
+                                    _ptr(Z), N, stream), "dyra_dense_forward")
+
+
+def dyra_dense_backward(p: int, dY, X, W, Z, act: int, dZ, dX, dW, dbias, N: int, stream) -> None:
+    _check(lib().dyra_dense_backward(p, _ptr(dY), _ptr(X), _ptr(W), _ptr(Z), act, _ptr(dZ),
+                                     _ptr(dX), _ptr(dW), _ptr(dbias), N, stream),
+           "dyra_dense_backward")
+
+
+def dyra_dense_status(p: int) -> int:
+    return _check(lib().dyra_dense_status(p), "dyra_dense_status")
+
+
+def dyra_dense_device_bytes(p: int) -> int:
+    return int(lib().dyra_dense_device_bytes(p))
+
+
+def dyra_dense_destroy(p: int) -> None:
+    _check(lib().dyra_dense_destroy(p), "dyra_dense_destroy")
+
+
+def dyra_moe_create(d_model: int, d_ff: int, experts: int, top_k: int, act: int, renorm: int,
+                    dtype: int) -> int:
+    h = ctypes.c_void_p()
+    _check(lib().dyra_moe_create(ctypes.byref(h), d_model, d_ff, experts, top_k, act, renorm,
+                                 dtype), "dyra_moe_create")
+    return h.value
+
+
+def dyra_moe_route(p: int, X, Wr, ids, weights, N: int, stream) -> None:
+    _check(lib().dyra_moe_route(p, _ptr(X), _ptr(Wr), _ptr(ids), _ptr(weights), N, stream),
+           "dyra_moe_route")
+
+
+def dyra_moe_experts(p: int, X, ids, weights, Wgu, Wd, residual, Y, N: int, stream) -> None:
+    _check(lib().dyra_moe_experts(p, _ptr(X), _ptr(ids), _ptr(weights), _ptr(Wgu), _ptr(Wd),
+                                  _ptr(residual), _ptr(Y), N, stream), "dyra_moe_experts")
+
+
+def dyra_moe_forward(p: int, X, Wr, Wgu, Wd, residual, Y, ids, weights, N: int, stream) -> None:
+    _check(lib().dyra_moe_forward(p, _ptr(X), _ptr(Wr), _ptr(Wgu), _ptr(Wd), _ptr(residual),
+                                  _ptr(Y), _ptr(ids), _ptr(weights), N, stream),
+           "dyra_moe_forward")
+
+
+def dyra_moe_status(p: int) -> int:
+    return _check(lib().dyra_moe_status(p), "dyra_moe_status")
+
+
+def dyra_moe_device_bytes(p: int) -> int:
+    return int(lib().dyra_moe_device_bytes(p))
+
+
+def dyra_moe_destroy(p: int) -> None:
+    _check(lib().dyra_moe_destroy(p), "dyra_moe_destroy")
+
+
+# ---- convenience objects ----
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError("act must be one of %s, not %r" % (", ".join(ACTIVATIONS), act))
+    return ACTIVATIONS[act]
+
+
+class _Layer:
+    """What both layers share: type, device, checks of tensors, streams."""
+
+    def _setup(self, dtype: str) -> int:
+        import torch
+        if dtype not in ("bf16", "f32"):
+            raise ValueError("dtype must be 'bf16' or 'f32', not %r" % (dtype,))
+        self.dtype = dtype
+        self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+        self.handle = None
+        return DYRA_BF16 if dtype == "bf16" else DYRA_F32
+
+    def _bind(self, handle: int) -> None:
+        import torch
+        self.handle = handle
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _need(self, name, t, *shape, dtype=None):
+        dtype = dtype or self.torch_dtype
+        if t is None or t.device != self.device or t.dtype != dtype or tuple(t.shape) != shape \
+                or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                             % (name, dtype, shape, self.device))
+
+    def _may(self, name, t, *shape):
+        if t is not None:
+            self._need(name, t, *shape)
+
+    def _rows(self, X, width, name="X"):
+        if X is None or X.dim() != 2:
+            raise ValueError("%s must be a matrix of %d columns" % (name, width))
+        self._need(name, X, X.shape[0], width)
+        return X.shape[0]
+
+    def _on(self, stream):
+        """(context in which results are allocated, the cudaStream_t)"""
+        import torch
+        if stream is None:
+            return contextlib.nullcontext(), torch.cuda.current_stream(self.device).cuda_stream
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        return torch.cuda.stream(stream), stream.cuda_stream
+
+    def _new(self, *shape, dtype=None):
+        import torch
+        return torch.empty(shape, device=self.device, dtype=dtype or self.torch_dtype)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class DenseLinear(_Layer):
+    """One dense linear layer shape on the current CUDA device."""
+
+    def __init__(self, d_in: int, d_out: int, dtype: str = "bf16"):
+        code = self._setup(dtype)
+        self.d_in, self.d_out = d_in, d_out
+        self._bind(dyra_dense_create(d_in, d_out, code))
+
+    def forward(self, X, W, bias=None, residual=None, act: str = "none", save_z: bool = False,
+                Y=None, stream=None):
+        """Y = act(X W^T + bias) + residual; with save_z the pair (Y, Z), Z the
+        pre-activations that backward() takes. Y may be given, and may be the
+        residual itself."""
+        code = _activation(act)
+        N = self._rows(X, self.d_in)
+        self._need("W", W, self.d_out, self.d_in)
+        self._may("bias", bias, self.d_out)
+        self._may("residual", residual, N, self.d_out)
+        self._may("Y", Y, N, self.d_out)
+        ctx, s = self._on(stream)
+        with ctx:
+            if Y is None:
+                Y = self._new(N, self.d_out)
+            Z = self._new(N, self.d_out) if save_z else None
+        dyra_dense_forward(self.handle, X, W, bias, residual, code, Y, Z, N, s)
+        return (Y, Z) if save_z else Y
+
+    def backward(self, dY, X, W, Z=None, act: str = "none", need_dX: bool = True,
+                 need_dW: bool = True, need_dbias: bool = True, stream=None):
+        """(dX, dW, dbias) from dY (None where not needed); the gradient of the
+        residual is dY. Z: the forward's pre-activations, unless act is 'none'.
+        X is not read without dW, W not without dX."""
+        code = _activation(act)
+        N = self._rows(dY, self.d_out, "dY")
+        if need_dW or X is not None:
+            self._need("X", X, N, self.d_in)
+        if need_dX or W is not None:
+            self._need("W", W, self.d_out, self.d_in)
+        if code != DYRA_ACT_NONE:
+            self._need("Z", Z, N, self.d_out)
+        ctx, s = self._on(stream)
+        with ctx:
+            dX = self._new(N, self.d_in) if need_dX else None
+            dW = self._new(self.d_out, self.d_in) if need_dW else None
+            dbias = self._new(self.d_out) if need_dbias else None
+            dZ = self._new(N, self.d_out) if code != DYRA_ACT_NONE else None
+            # freed on return; the allocator hands it out again in stream order
+        dyra_dense_backward(self.handle, dY, X, W, Z, code, dZ, dX, dW, dbias, N, s)
+        return dX, dW, dbias
+
+    def status(self) -> int:
+        return dyra_dense_status(self.handle)
+
+    def device_bytes(self) -> int:
+        return dyra_dense_device_bytes(self.handle)
+
+    def close(self) -> None:
+        if self.handle:
+            dyra_dense_destroy(self.handle)
+            self.handle = None
+
+
+class MoeLayer(_Layer):
+    """One mixture-of-experts layer shape on the current CUDA device: gated
+    experts d_model -> d_ff -> d_model, top_k of them per token."""
+
+    def __init__(self, d_model: int, d_ff: int, experts: int, top_k: int, dtype: str = "bf16",
+                 act: str = "silu", renorm: bool = True):
+        code = self._setup(dtype)
+        self.d_model, self.d_ff, self.experts_n, self.top_k = d_model, d_ff, experts, top_k
+        self._bind(dyra_moe_create(d_model, d_ff, experts, top_k, _activation(act),
+                                   int(bool(renorm)), code))
+
+    def _need_experts(self, Wgu, Wd):
+        self._need("Wgu", Wgu, self.experts_n, 2 * self.d_ff, self.d_model)
+        self._need("Wd", Wd, self.experts_n, self.d_model, self.d_ff)
+
+    def route(self, X, Wr, stream=None):
+        """(ids, weights): each token's top_k experts, largest logit first (the
+        lower index among equals), and their softmax weights."""
+        import torch
+        N = self._rows(X, self.d_model)
+        self._need("Wr", Wr, self.experts_n, self.d_model)
+        ctx, s = self._on(stream)
+        with ctx:
+            ids = self._new(N, self.top_k, dtype=torch.int32)
+            weights = self._new(N, self.top_k, dtype=torch.float32)
+        dyra_moe_route(self.handle, X, Wr, ids, weights, N, s)
+        return ids, weights
+
+    def experts(self, X, ids, weights, Wgu, Wd, residual=None, Y=None, stream=None):
+        """sum over k of weights[n][k] * expert ids[n][k] of token n, + residual.
+        Ids outside the experts (such as -1) add nothing."""
+        import torch
+        N = self._rows(X, self.d_model)
+        self._need("ids", ids, N, self.top_k, dtype=torch.int32)
+        self._need("weights", weights, N, self.top_k, dtype=torch.float32)
+        self._need_experts(Wgu, Wd)
+        self._may("residual", residual, N, self.d_model)
+        self._may("Y", Y, N, self.d_model)
+        ctx, s = self._on(stream)
+        with ctx:
+            if Y is None:
+                Y = self._new(N, self.d_model)
+        dyra_moe_experts(self.handle, X, ids, weights, Wgu, Wd, residual, Y, N, s)
+        return Y
+
+    def forward(self, X, Wr, Wgu, Wd, residual=None, Y=None, stream=None):
+        """The whole layer: (Y, ids, weights)."""
+        import torch
+        N = self._rows(X, self.d_model)
+        self._need("Wr", Wr, self.experts_n, self.d_model)
+        self._need_experts(Wgu, Wd)
+        self._may("residual", residual, N, self.d_model)
+        self._may("Y", Y, N, self.d_model)
+        ctx, s = self._on(stream)
+        with ctx:
+            ids = self._new(N, self.top_k, dtype=torch.int32)
+            weights = self._new(N, self.top_k, dtype=torch.float32)
+            if Y is None:
+                Y = self._new(N, self.d_model)
+        dyra_moe_forward(self.handle, X, Wr, Wgu, Wd, residual, Y, ids, weights, N, s)
+        return Y, ids, weights
+
+    def status(self) -> int:
+        return dyra_moe_status(self.handle)
+
+    def device_bytes(self) -> int:
+        return dyra_moe_device_bytes(self.handle)
+
+    def close(self) -> None:
+        if self.handle:
+            dyra_moe_destroy(self.handle)
+            self.handle = None
