@@ -63,7 +63,7 @@ int dyra_dense_create(dyra_dense_t *out, int d_in, int d_out, dyra_dtype_t dtype
  *              type (the Z of dyra_dense_backward), or NULL
  * Z is kept in fp32 inside the call: act and residual are applied before the
  * one rounding of Y. N == 0 is a no-op.
- * Errors: DYRA_ERR_INVALID_ARG (NULL handle, X, W or Y; N < 0 or > 2^31 - 1;
+ * Errors: DYRA_ERR_INVALID_ARG (NULL handle, X, W or Y; N < 0 or > 2^31 - 512;
  * unknown act), DYRA_ERR_ALIGNMENT, DYRA_ERR_CUDA.
  */
 int dyra_dense_forward(dyra_dense_t p, const void *X, const void *W, const void *bias,

@@ -34,6 +34,10 @@ struct LinearGemm {
 template <typename T>
 int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 
+// Tensor-core product of bf16 operands (layers_umma.cu). pdl: a programmatic
+// dependent launch behind the grid before it in the stream.
+int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl);
+
 // dZ = dY act'(Z) (skipped for DYRA_ACT_NONE) and its column sums (skipped
 // when dbias is NULL). partial: kColSumChunks x d_out floats; counters:
 // col_sum_blocks(d_out) ints, zero before and after the call.

@@ -38,7 +38,8 @@ struct dyra_moe {
 
 namespace {
 
-constexpr int64_t kMaxRows = (static_cast<int64_t>(1) << 31) - 1;
+// tile origins up to 511 rows beyond the last stay inside 32-bit coordinates
+constexpr int64_t kMaxRows = (static_cast<int64_t>(1) << 31) - 512;
 
 bool simt_requested() {
   const char* kv = std::getenv("DYRA_KERNELS");
@@ -88,9 +89,10 @@ int launched(int rc) {
   return DYRA_ERR_CUDA;
 }
 
-int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s) {
+int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s, bool pdl) {
   if (p->dtype == DYRA_F32) return launch_linear_simt<float>(g, p->dev, s);
-  return launch_linear_simt<__nv_bfloat16>(g, p->dev, s);
+  if (p->simt) return launch_linear_simt<__nv_bfloat16>(g, p->dev, s);
+  return launch_linear_umma(g, p->dev, s, pdl);
 }
 
 template <class T>
@@ -190,7 +192,7 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   g.Out = Y;
   g.Z = Z;
   g.status = p->status;
-  return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream), false));
 }
 
 int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const void* W,
@@ -230,7 +232,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
     g.J = N;
     g.K = p->d_out;
     g.Out = dX;
-    const int rc = linear(p, g, s);
+    const int rc = linear(p, g, s, has_act || dbias);
     if (rc) return launched(rc);
   }
   if (dW) {
@@ -239,7 +241,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
     g.J = p->d_out;
     g.K = N;
     g.Out = dW;
-    const int rc = linear(p, g, s);
+    const int rc = linear(p, g, s, has_act || dbias || dX);
     if (rc) return launched(rc);
   }
   return DYRA_OK;

@@ -59,14 +59,25 @@ __device__ __forceinline__ float act_grad_f(float z) {
   return 1.f;
 }
 
-// Calls f(std::integral_constant-like tag) for the run-time activation, so
-// that loops over values hold one activation's code.
+// Calls f with a tag for the run-time activation, so that loops over values
+// hold one activation's code.
 template <int V>
 struct ActTag {
   static constexpr int value = V;
 };
 template <class F>
-__host__ __device__ __forceinline__ void with_act(int act, const F& f) {
+__device__ __forceinline__ void with_act(int act, const F& f) {
+  switch (act) {
+    case DYRA_ACT_RELU: f(ActTag<DYRA_ACT_RELU>()); break;
+    case DYRA_ACT_GELU: f(ActTag<DYRA_ACT_GELU>()); break;
+    case DYRA_ACT_GELU_TANH: f(ActTag<DYRA_ACT_GELU_TANH>()); break;
+    case DYRA_ACT_SILU: f(ActTag<DYRA_ACT_SILU>()); break;
+    default: f(ActTag<DYRA_ACT_NONE>()); break;
+  }
+}
+// The same on the host, around launches.
+template <class F>
+inline void with_act_host(int act, const F& f) {
   switch (act) {
     case DYRA_ACT_RELU: f(ActTag<DYRA_ACT_RELU>()); break;
     case DYRA_ACT_GELU: f(ActTag<DYRA_ACT_GELU>()); break;

@@ -205,7 +205,7 @@ int launch_act_backward_v(const T* dY, const T* Z, int act, T* dZ, T* dbias, int
   const int64_t want = std::max<int64_t>(1, 4 * dev.sm_count / cols);
   const int chunks = static_cast<int>(
       std::min<int64_t>({want, std::max<int64_t>(1, (N + 7) / 8), kColSumChunks}));
-  with_act(act, [&](auto tag) {
+  with_act_host(act, [&](auto tag) {
     act_backward_kernel<T, V, decltype(tag)::value><<<dim3(cols, chunks), 256, 0, s>>>(
         dY, Z, dZ, dbias, N, d_out, partial, counters, status);
   });
