@@ -53,23 +53,33 @@ struct DeviceGuard {
   }
 };
 
-// The current device's properties; DYRA_ERR_UNSUPPORTED unless it is a B200.
+// The current device's attributes (each a lookup of microseconds, where the
+// whole property structure takes milliseconds); DYRA_ERR_UNSUPPORTED unless it
+// is a B200.
 inline int current_device_info(DeviceInfo* info) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return DYRA_ERR_CUDA;
   }
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return DYRA_ERR_CUDA;
-  if (prop.major != 10 || prop.minor != 0) return DYRA_ERR_UNSUPPORTED;
+  int v[6];
+  const cudaDeviceAttr attr[6] = {
+      cudaDevAttrMultiProcessorCount,       cudaDevAttrMaxSharedMemoryPerBlockOptin,
+      cudaDevAttrMaxSharedMemoryPerMultiprocessor, cudaDevAttrReservedSharedMemoryPerBlock,
+      cudaDevAttrComputeCapabilityMajor,    cudaDevAttrComputeCapabilityMinor};
+  for (int i = 0; i < 6; ++i)
+    if (cudaDeviceGetAttribute(&v[i], attr[i], dev) != cudaSuccess) {
+      cudaGetLastError();
+      return DYRA_ERR_CUDA;
+    }
+  if (v[4] != 10 || v[5] != 0) return DYRA_ERR_UNSUPPORTED;
   info->device = dev;
-  info->sm_count = prop.multiProcessorCount;
-  info->max_smem_optin = static_cast<int>(prop.sharedMemPerBlockOptin);
-  info->smem_per_sm = static_cast<int>(prop.sharedMemPerMultiprocessor);
-  info->smem_reserved = static_cast<int>(prop.reservedSharedMemPerBlock);
-  info->cc_major = prop.major;
-  info->cc_minor = prop.minor;
+  info->sm_count = v[0];
+  info->max_smem_optin = v[1];
+  info->smem_per_sm = v[2];
+  info->smem_reserved = v[3];
+  info->cc_major = v[4];
+  info->cc_minor = v[5];
   return DYRA_OK;
 }
 

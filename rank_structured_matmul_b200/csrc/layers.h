@@ -28,6 +28,8 @@ struct LinearGemm {
   void* Out = nullptr;
   void* Z = nullptr;
   int* status = nullptr;
+  float* ws = nullptr;      // tensor cores: linear_ws_bytes of scratch
+  int* counters = nullptr;  // tensor cores: linear_counters ints, zero between calls
 };
 
 // CUDA-core product (layers_simt.cu): T = float or __nv_bfloat16.
@@ -37,6 +39,8 @@ int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t 
 // Tensor-core product of bf16 operands (layers_umma.cu). pdl: a programmatic
 // dependent launch behind the grid before it in the stream.
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl);
+size_t linear_ws_bytes(const DeviceInfo& dev);
+int linear_counters(int d_in, int d_out, const DeviceInfo& dev);
 
 // dZ = dY act'(Z) (skipped for DYRA_ACT_NONE) and its column sums (skipped
 // when dbias is NULL). partial: kColSumChunks x d_out floats; counters:
@@ -66,5 +70,18 @@ template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
                             const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
                             float* part, int* status, cudaStream_t s);
+
+// Tensor-core experts for N <= kMoeTokens tokens (layers_moe_umma.cu). hidden:
+// moe_reached_max x kMoeTokens x f values; ws and counters (zero between calls)
+// as the sizes below. pdl: launched behind the router's grid.
+int moe_reached_max(const MoeShape& m);
+int moe_counters(const MoeShape& m);
+size_t moe_ws_bytes(const DeviceInfo& dev);
+int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int* ids,
+                            const float* weights, const __nv_bfloat16* Wgu,
+                            const __nv_bfloat16* Wd, const __nv_bfloat16* residual,
+                            __nv_bfloat16* Y, int N, __nv_bfloat16* hidden, float* ws,
+                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s,
+                            bool pdl);
 
 }  // namespace dyra

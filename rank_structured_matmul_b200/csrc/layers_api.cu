@@ -21,8 +21,11 @@ struct dyra_dense {
   bool simt = false;        // fp32, or DYRA_KERNELS=simt (debugging)
   float* colsum = nullptr;  // kColSumChunks x d_out partial column sums
   int* counters = nullptr;  // col_sum_blocks(d_out) arrival counters, zero between calls
+  float* ws = nullptr;      // tensor cores: parts of split tiles, and
+  int* tiles = nullptr;     // their arrival counters, zero between calls
   int* status = nullptr;
   size_t bytes = 0;
+  int n_tiles = 0;
 };
 
 struct dyra_moe {
@@ -31,9 +34,11 @@ struct dyra_moe {
   DeviceInfo dev;
   bool simt = false;
   void* hidden = nullptr;  // the hidden values of one group of kMoeTokens tokens
-  float* part = nullptr;   // CUDA cores: its slots' outputs
+  float* part = nullptr;   // CUDA cores: its slots' outputs; tensor cores: parts of split tiles
+  int* tiles = nullptr;    // tensor cores: the tiles' arrival counters, zero between calls
   int* status = nullptr;
   size_t bytes = 0;
+  int n_tiles = 0;
 };
 
 namespace {
@@ -72,12 +77,14 @@ void give(T*& p) {
   p = nullptr;
 }
 
-int read_status(const DeviceInfo& dev, int* status) {
+// A call that gave up may leave arrival counters behind: they start again.
+int read_status(const DeviceInfo& dev, int* status, int* tiles, int n_tiles) {
   DeviceGuard g(dev.device);
   if (!g.ok || cudaDeviceSynchronize() != cudaSuccess) return DYRA_ERR_CUDA;
   int st = 0;
   if (cudaMemcpy(&st, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
       cudaMemset(status, 0, sizeof(int)) != cudaSuccess ||
+      (st != 0 && tiles && cudaMemset(tiles, 0, sizeof(int) * n_tiles) != cudaSuccess) ||
       cudaStreamSynchronize(nullptr) != cudaSuccess)
     return DYRA_ERR_CUDA;
   return st;
@@ -106,6 +113,8 @@ int act_backward(const dyra_dense* p, const void* dY, const void* Z, int act, vo
 void dense_free(dyra_dense* p) {
   give(p->colsum);
   give(p->counters);
+  give(p->ws);
+  give(p->tiles);
   give(p->status);
   delete p;
 }
@@ -113,6 +122,7 @@ void dense_free(dyra_dense* p) {
 void moe_free(dyra_moe* p) {
   give(p->hidden);
   give(p->part);
+  give(p->tiles);
   give(p->status);
   delete p;
 }
@@ -126,8 +136,15 @@ int moe_route(const dyra_moe* p, const void* X, const void* Wr, int32_t* ids, fl
 
 template <class T>
 int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const float* weights,
-                const void* Wgu, const void* Wd, const void* residual, void* Y, int n,
+                const void* Wgu, const void* Wd, const void* residual, void* Y, int n, bool pdl,
                 cudaStream_t s) {
+  if constexpr (sizeof(T) == 2)
+    if (!p->simt)
+      return launch_moe_experts_umma(p->m, static_cast<const T*>(X), ids, weights,
+                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
+                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
+                                     static_cast<T*>(p->hidden), p->part, p->tiles, p->status,
+                                     p->dev, s, pdl);
   return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
@@ -138,6 +155,36 @@ int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
 int moe_check(const dyra_moe* p, int64_t N) {
   if (p == nullptr || N < 0 || N > kMaxRows) return DYRA_ERR_INVALID_ARG;
   return DYRA_OK;
+}
+
+// after_route: the router's grid is the one before in the stream.
+int run_experts(const dyra_moe* p, const void* X, const int32_t* ids, const float* weights,
+                const void* Wgu, const void* Wd, const void* residual, void* Y, int64_t N,
+                bool after_route, cudaStream_t s) {
+  int rc = moe_check(p, N);
+  if (rc || N == 0) return rc;
+  if (X == nullptr || ids == nullptr || weights == nullptr || Wgu == nullptr || Wd == nullptr ||
+      Y == nullptr)
+    return DYRA_ERR_INVALID_ARG;
+  for (const void* q : {X, static_cast<const void*>(ids), static_cast<const void*>(weights), Wgu,
+                        Wd, residual, static_cast<const void*>(Y)})
+    if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  DeviceGuard g(p->dev.device);
+  if (!g.ok) return DYRA_ERR_CUDA;
+  const size_t row = elem_size(p->dtype) * p->m.d;
+  for (int64_t n0 = 0; n0 < N && rc == 0; n0 += kMoeTokens) {
+    const int n = static_cast<int>(std::min<int64_t>(kMoeTokens, N - n0));
+    const void* x = static_cast<const char*>(X) + n0 * row;
+    const void* r = residual ? static_cast<const char*>(residual) + n0 * row : nullptr;
+    const bool pdl = after_route || n0 > 0;
+    void* y = static_cast<char*>(Y) + n0 * row;
+    rc = p->dtype == DYRA_F32
+             ? moe_experts<float>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k, Wgu, Wd,
+                                  r, y, n, pdl, s)
+             : moe_experts<__nv_bfloat16>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k,
+                                          Wgu, Wd, r, y, n, pdl, s);
+  }
+  return launched(rc);
 }
 
 }  // namespace
@@ -159,9 +206,12 @@ int dyra_dense_create(dyra_dense_t* out, int d_in, int d_out, dyra_dtype_t dtype
   p->dtype = dtype;
   p->dev = dev;
   p->simt = dtype == DYRA_F32 || simt_requested();
+  p->n_tiles = p->simt ? 0 : linear_counters(d_in, d_out, dev);
   if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
       (rc = take(&p->colsum, sizeof(float) * kColSumChunks * d_out, &p->bytes)) ||
-      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes))) {
+      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes)) ||
+      (!p->simt && (rc = take(&p->ws, linear_ws_bytes(dev), &p->bytes))) ||
+      (!p->simt && (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes)))) {
     dense_free(p);
     return rc;
   }
@@ -192,6 +242,8 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   g.Out = Y;
   g.Z = Z;
   g.status = p->status;
+  g.ws = p->ws;
+  g.counters = p->tiles;
   return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream), false));
 }
 
@@ -224,6 +276,8 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
   }
   LinearGemm g;
   g.status = p->status;
+  g.ws = p->ws;
+  g.counters = p->tiles;
   g.B = has_act ? dZ : dY;
   g.M = p->d_in;
   if (dX) {
@@ -248,7 +302,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
 }
 
 int dyra_dense_status(dyra_dense_t p) {
-  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status);
+  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status, p->tiles, p->n_tiles);
 }
 
 size_t dyra_dense_device_bytes(dyra_dense_t p) { return p == nullptr ? 0 : p->bytes; }
@@ -280,9 +334,14 @@ int dyra_moe_create(dyra_moe_t* out, int d_model, int d_ff, int experts, int top
   p->dev = dev;
   p->simt = dtype == DYRA_F32 || simt_requested();
   const size_t slots = static_cast<size_t>(kMoeTokens) * top_k;
+  const size_t hidden_rows =
+      p->simt ? slots : static_cast<size_t>(kMoeTokens) * moe_reached_max(p->m);
+  const size_t part_bytes = p->simt ? slots * d_model * sizeof(float) : moe_ws_bytes(dev);
+  p->n_tiles = p->simt ? 0 : moe_counters(p->m);
   if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
-      (rc = take(&p->hidden, slots * d_ff * elem_size(dtype), &p->bytes)) ||
-      (rc = take(&p->part, slots * d_model * sizeof(float), &p->bytes))) {
+      (rc = take(&p->hidden, hidden_rows * d_ff * elem_size(dtype), &p->bytes)) ||
+      (rc = take(&p->part, part_bytes, &p->bytes)) ||
+      (!p->simt && (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes)))) {
     moe_free(p);
     return rc;
   }
@@ -309,30 +368,8 @@ int dyra_moe_route(dyra_moe_t p, const void* X, const void* Wr, int32_t* ids, fl
 int dyra_moe_experts(dyra_moe_t p, const void* X, const int32_t* ids, const float* weights,
                      const void* Wgu, const void* Wd, const void* residual, void* Y, int64_t N,
                      dyra_stream_t stream) {
-  int rc = moe_check(p, N);
-  if (rc || N == 0) return rc;
-  if (X == nullptr || ids == nullptr || weights == nullptr || Wgu == nullptr || Wd == nullptr ||
-      Y == nullptr)
-    return DYRA_ERR_INVALID_ARG;
-  for (const void* q : {X, static_cast<const void*>(ids), static_cast<const void*>(weights), Wgu,
-                        Wd, residual, static_cast<const void*>(Y)})
-    if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
-  DeviceGuard g(p->dev.device);
-  if (!g.ok) return DYRA_ERR_CUDA;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t row = elem_size(p->dtype) * p->m.d;
-  for (int64_t n0 = 0; n0 < N && rc == 0; n0 += kMoeTokens) {
-    const int n = static_cast<int>(std::min<int64_t>(kMoeTokens, N - n0));
-    const void* x = static_cast<const char*>(X) + n0 * row;
-    const void* r = residual ? static_cast<const char*>(residual) + n0 * row : nullptr;
-    void* y = static_cast<char*>(Y) + n0 * row;
-    rc = p->dtype == DYRA_F32
-             ? moe_experts<float>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k, Wgu, Wd,
-                                  r, y, n, s)
-             : moe_experts<__nv_bfloat16>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k,
-                                          Wgu, Wd, r, y, n, s);
-  }
-  return launched(rc);
+  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, false,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dyra_moe_forward(dyra_moe_t p, const void* X, const void* Wr, const void* Wgu, const void* Wd,
@@ -346,11 +383,12 @@ int dyra_moe_forward(dyra_moe_t p, const void* X, const void* Wr, const void* Wg
     return DYRA_ERR_ALIGNMENT;
   rc = dyra_moe_route(p, X, Wr, ids, weights, N, stream);
   if (rc) return rc;
-  return dyra_moe_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, stream);
+  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, true,
+                     reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dyra_moe_status(dyra_moe_t p) {
-  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status);
+  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status, p->tiles, p->n_tiles);
 }
 
 size_t dyra_moe_device_bytes(dyra_moe_t p) { return p == nullptr ? 0 : p->bytes; }

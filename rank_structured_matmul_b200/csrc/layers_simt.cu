@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(256)
         float z = acc[j][m];
         if (bias) z += load_f(bias[gm]);
         if (Z) Z[at] = store_f<T>(z);
-        float y = act_f<ACT>(z);
+        float y = act_f<ACT, kFastMath<T>>(z);
         if (residual) y += load_f(residual[at]);
         Out[at] = store_f<T>(y);
       }
@@ -125,11 +125,6 @@ int launch_linear_simt_g(const LinearGemm& g, cudaStream_t s) {
 // aligned, else single values) and every 8 x chunks-th row; the sums of its 8
 // row lanes meet in shared memory, the chunks' sums in `partial`, and the last
 // block of a column group to arrive adds the chunks in order and rounds once.
-template <typename T, int V>
-struct Piece {
-  T v[V];
-};
-
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(256)
     act_backward_kernel(const T* dY, const T* Z, T* dZ, T* __restrict__ dbias, int64_t N, int d_out,
@@ -154,7 +149,7 @@ __global__ void __launch_bounds__(256)
           // a zero slope of the ReLU is a zero gradient, whatever dY holds
           const float d = ACT == DYRA_ACT_RELU
                               ? (load_f(z.v[i]) > 0.f ? load_f(g.v[i]) : 0.f)
-                              : load_f(g.v[i]) * act_grad_f<ACT>(load_f(z.v[i]));
+                              : load_f(g.v[i]) * act_grad_f<ACT, kFastMath<T>>(load_f(z.v[i]));
           sum[i] += d;
           out.v[i] = store_f<T>(d);
         }
@@ -223,6 +218,7 @@ __global__ void __launch_bounds__(256)
     moe_route_kernel(MoeShape m, const T* __restrict__ X, const T* __restrict__ Wr,
                      int* __restrict__ ids, float* __restrict__ weights) {
   __shared__ double logit[DYRA_MOE_MAX_EXPERTS];
+  sm100::pdl_launch_dependents();  // the experts' kernel may set up meanwhile
   const int64_t n = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* x = X + n * m.d;
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(256)
         if (!sm100::in_bounds(status, at, 1, static_cast<size_t>(slots) * rows)) continue;
         if (STAGE == 0)
           with_act(act, [&](auto tag) {
-            hidden[at] = store_f<T>(act_f<decltype(tag)::value>(a0[q]) * a1[q]);
+            hidden[at] = store_f<T>(act_f<decltype(tag)::value, kFastMath<T>>(a0[q]) * a1[q]);
           });
         else
           part[at] = a0[q];

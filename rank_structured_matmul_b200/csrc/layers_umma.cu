@@ -5,6 +5,7 @@
 
 #include "layers.h"
 #include "layers_math.cuh"
+#include "stream_gemm.cuh"
 #include "umma_common.cuh"
 
 namespace dyra {
@@ -160,7 +161,7 @@ struct DensePairPolicy {
       }
       if (p.keep_z) emit(v, &p.tmZ, x, y0, e);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = act_f<ACT>(v[i]);
+      for (int i = 0; i < 64; ++i) v[i] = act_f<ACT, true>(v[i]);
       if (p.residual) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) add8(v + 8 * c, rq[c]);
@@ -211,12 +212,200 @@ int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool
   return launch_gemm_pair<Pol>(p, smem, dev, s, pdl);
 }
 
+// ---------------------------------------------------------------- streams ----
+// The same products where the 256 x 256 tiles are few (stream_gemm.cuh): a tile
+// is 128 columns m of the output (A's rows) x nb rows j, so a thread holds one m
+// and a warp's stores of one j are 64 contiguous bytes.
+struct DenseStreamParams {
+  StreamCommon c;
+  CUtensorMap tmA, tmB;
+  int M, J, K, tiles_j;
+  int act;
+  const __nv_bfloat16* bias;
+  const __nv_bfloat16* residual;  // may be Out
+  __nv_bfloat16* Out;
+  __nv_bfloat16* Z;
+};
+
+template <bool kAMn, bool kBMn, bool kEpi>
+struct DenseStreamPolicy {
+  using Params = DenseStreamParams;
+  struct Acc {};
+  static constexpr uint32_t kSmemBytes = 0;
+  static constexpr uint64_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;
+
+  static __device__ __forceinline__ void prefetch(const Params& p) {
+    tma_prefetch_desc(&p.tmA);
+    tma_prefetch_desc(&p.tmB);
+  }
+  static __device__ __forceinline__ void setup(const Params&, uint8_t*) {}
+  static __device__ __forceinline__ void shape(const Params& p, uint8_t*, int& tiles, int& nsub,
+                                               int& ks) {
+    tiles = ceil_div_dev(p.M, 128) * p.tiles_j;
+    nsub = 1;
+    ks = ceil_div_dev(p.K, 64);
+  }
+  // tiles of the same rows of A are neighbours: they share A through L2
+  static __device__ __forceinline__ int m_of(const Params& p, int tile) {
+    return tile / p.tiles_j * 128;
+  }
+  static __device__ __forceinline__ int j_of(const Params& p, int tile) {
+    return tile % p.tiles_j * p.c.nb;
+  }
+  static __device__ __forceinline__ void load_a(const Params& p, uint8_t*, int tile, int, int k,
+                                                uint32_t dst, uint32_t bar) {
+    const int m = m_of(p, tile);
+    if (kAMn) {
+      tma_load_2d(dst, &p.tmA, bar, m, k * 64);
+      tma_load_2d(dst + 8192u, &p.tmA, bar, m + 64, k * 64);
+    } else {
+      tma_load_2d(dst, &p.tmA, bar, k * 64, m);
+    }
+  }
+  static __device__ __forceinline__ void load_b(const Params& p, uint8_t*, int tile, int, int k,
+                                                uint32_t dst, uint32_t bar) {
+    const int j = j_of(p, tile);
+    if (kBMn) {
+      for (int q = 0; q < p.c.nb; q += 64)
+        tma_load_2d(dst + static_cast<uint32_t>(q) * 128u, &p.tmB, bar, j + q, k * 64);
+    } else {
+      tma_load_2d(dst, &p.tmB, bar, k * 64, j);
+    }
+  }
+  static __device__ __forceinline__ uint64_t adesc(uint32_t a) {
+    return kAMn ? mnmajor_desc(a, 0) : kmajor_desc(a, 0);
+  }
+  static __device__ __forceinline__ uint64_t bdesc(uint32_t b) {
+    return kBMn ? mnmajor_desc(b, 0) : kmajor_desc(b, 0);
+  }
+  // Columns col0 .. col0 + n - 1 of the tile, this thread's row: out.
+  template <int ACT>
+  static __device__ __forceinline__ void finish(const Params& p, int j0, int m, float bias,
+                                                const float (&v)[32], int n) {
+    if (m >= p.M) return;
+    const size_t extent = static_cast<size_t>(p.J) * p.M;
+    float r[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const size_t at = static_cast<size_t>(j0 + i) * p.M + m;
+      r[i] = kEpi && p.residual && i < n && in_bounds(p.c.status, at, 1, extent)
+                 ? __bfloat162float(p.residual[at])
+                 : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i >= n) break;
+      const size_t at = static_cast<size_t>(j0 + i) * p.M + m;
+      if (!in_bounds(p.c.status, at, 1, extent)) continue;
+      const float z = v[i] + bias;
+      if (kEpi && p.Z) p.Z[at] = __float2bfloat16_rn(z);
+      p.Out[at] = __float2bfloat16_rn(act_f<ACT, true>(z) + r[i]);
+    }
+  }
+  template <class Release>
+  static __device__ __forceinline__ void segment(const Params& p, uint8_t*, const StreamSeg& s,
+                                                 int per_tile, uint32_t tacc, StreamEpi& e, Acc&,
+                                                 const Release& release) {
+    const int j0 = j_of(p, s.tile), m = m_of(p, s.tile) + e.row;
+    const int n = min(p.c.nb, p.J - j0);
+    const float bias = kEpi && p.bias && m < p.M ? __bfloat162float(p.bias[m]) : 0.f;
+    auto out = [&](const float(&v)[32], int col) {
+      if (kEpi)
+        with_act(p.act, [&](auto tag) {
+          finish<decltype(tag)::value>(p, j0 + col, m, bias, v, n - col);
+        });
+      else
+        finish<DYRA_ACT_NONE>(p, j0 + col, m, bias, v, n - col);
+    };
+    float* part = stream_part(p.c, static_cast<int>(blockIdx.x), s.first) + e.row;
+    for (int col = 0; col < n; col += 32) {
+      __syncwarp();
+      uint32_t raw[32];
+      tmem_ld_32x32b_x32(tacc + col, raw);
+      tmem_ld_wait();
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = f32(raw[i]);
+      if (s.whole) {
+        out(v, col);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (col + i < n) part[(col + i) * 128] = v[i];
+      }
+    }
+    release();
+    if (s.whole) return;
+    int c0, c1;
+    if (!stream_arrive(p.c, s, per_tile, e, c0, c1)) return;
+    for (int col = 0; col < n; col += 32) {
+      float v[32];
+      stream_sum(p.c, c0, c1, e.row, col, n - col, v);
+      out(v, col);
+    }
+  }
+  static __device__ __forceinline__ void nothing(const Params&, const StreamEpi&) {}
+};
+
+template <bool kAMn, bool kBMn, bool kEpi>
+int launch_stream(const LinearGemm& g, int nb, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+  using Pol = DenseStreamPolicy<kAMn, kBMn, kEpi>;
+  DenseStreamParams p;
+  p.M = static_cast<int>(g.M);
+  p.J = static_cast<int>(g.J);
+  p.K = static_cast<int>(g.K);
+  p.tiles_j = ceil_div(g.J, nb);
+  p.act = g.act;
+  p.bias = static_cast<const __nv_bfloat16*>(g.bias);
+  p.residual = static_cast<const __nv_bfloat16*>(g.residual);
+  p.Out = static_cast<__nv_bfloat16*>(g.Out);
+  p.Z = static_cast<__nv_bfloat16*>(g.Z);
+  if (!(kAMn ? encode_2d(&p.tmA, g.A, g.M, g.K, 64) : encode_2d(&p.tmA, g.A, g.K, g.M, 128)) ||
+      !(kBMn ? encode_2d(&p.tmB, g.B, g.J, g.K, 64)
+             : encode_2d(&p.tmB, g.B, g.K, g.J, static_cast<uint32_t>(nb))))
+    return -2;
+  const uint32_t smem =
+      stream_setup<Pol>(p.c, nb, kAMn, kBMn, g.ws, g.counters, g.status, dev);
+  if (!smem) return -3;
+  return stream_launch<Pol>(p, smem, dev, s, pdl);
+}
+
+// Columns of a stream tile for the product, 0: the CTA pairs take it.
+int stream_columns(const LinearGemm& g, const DeviceInfo& dev) {
+  const int64_t pair_tiles =
+      static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
+  if (g.J > kStreamMaxNb && pair_tiles > dev.sm_count / 2) return 0;
+  const int tj = ceil_div(g.J, kStreamMaxNb);
+  int nb = ceil_div(ceil_div(g.J, tj), 16) * 16;
+  if (g.b_mn) nb = nb <= 64 ? 64 : 128;  // whole boxes of 64
+  // steps are counted in 32 bits
+  if (static_cast<double>(ceil_div(g.M, 128)) * ceil_div(g.J, nb) * ceil_div(g.K, 64) > 1e9)
+    return 0;
+  return nb;
+}
+
 }  // namespace
 
+size_t linear_ws_bytes(const DeviceInfo& dev) {
+  return static_cast<size_t>(dev.sm_count) * 2 * kStreamMaxNb * 128 * sizeof(float);
+}
+
+// Tiles of a stream: one per 128 columns m of up to kStreamMaxNb rows, or where
+// the pairs' tiles are at most half the SMs, four of 128 x 128 for each of those.
+int linear_counters(int d_in, int d_out, const DeviceInfo& dev) {
+  return std::max(ceil_div(std::max(d_in, d_out), 128), dev.sm_count / 2 * 4);
+}
+
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  if (g.a_mn && g.b_mn) return launch_pair<true, true, false>(g, dev, s, pdl);
-  if (g.a_mn) return launch_pair<false, true, false>(g, dev, s, pdl);
-  return launch_pair<false, false, true>(g, dev, s, pdl);
+  const int nb = stream_columns(g, dev);
+  if (g.a_mn && g.b_mn)
+    return nb ? launch_stream<true, true, false>(g, nb, dev, s, pdl)
+              : launch_pair<true, true, false>(g, dev, s, pdl);
+  if (g.a_mn)
+    return nb ? launch_stream<true, false, false>(g, nb, dev, s, pdl)
+              : launch_pair<false, true, false>(g, dev, s, pdl);
+  return nb ? launch_stream<false, false, true>(g, nb, dev, s, pdl)
+            : launch_pair<false, false, true>(g, dev, s, pdl);
 }
 
 }  // namespace dyra
