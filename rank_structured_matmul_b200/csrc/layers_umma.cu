@@ -2,6 +2,7 @@
 // cores: fp32 accumulation in tensor memory, operands by TMA, the epilogue
 // (bias, activation, residual, the kept pre-activations) on the accumulator.
 #include <algorithm>
+#include <atomic>
 
 #include "layers.h"
 #include "layers_math.cuh"
@@ -19,6 +20,20 @@ __device__ __forceinline__ uint64_t mnmajor_desc(uint32_t base, int ks) {
   return smem_desc(base + static_cast<uint32_t>(ks) * 2048u, 8192u, 1024u, kLayoutSw128);
 }
 
+// v[0..8) += the eight bf16 values of q; eight values rounded to bf16
+__device__ __forceinline__ void add8(float* v, const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] += __uint_as_float(w[j] << 16);
+    v[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
 // ------------------------------------------------------------ CTA pairs ----
 // Out tile of 256 rows (j) x bn columns (m) on a CTA pair: CTA r loads rows
 // j0 + 128 r of the row operand and columns m0 + (bn / 2) r of the other, each
@@ -28,22 +43,35 @@ struct DensePairParams {
   CUtensorMap tmRow;  // row operand (J x K, or K x J when MN-major)
   CUtensorMap tmCol;  // column operand (M x K, or K x M when MN-major)
   CUtensorMap tmOut;  // J x M, box (64, 128), store
-  CUtensorMap tmZ;    // the same over the kept pre-activations
+  CUtensorMap tmZ;    // the same over the kept pre-activations, or the residual
   int J, M, K, bn, tiles_m;
-  int act, keep_z;
+  int act;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
 };
 
-// kEpi compiles the forward's epilogue in; the gradients' products store the
-// accumulator as it is.
-template <bool kRowMn, bool kColMn, bool kEpi>
+// What a pair kernel is compiled with: the gradients' products store the
+// accumulator as it is; the forward adds bias and activation, and either the
+// kept pre-activations (with a residual read row by row, if there is one) or a
+// residual that comes by TMA into the store boxes.
+enum PairEpilogue { kPlain, kForward, kForwardZ, kForwardResidual };
+
+template <bool kRowMn, bool kColMn, PairEpilogue kMode>
 struct DensePairPolicy {
+  static constexpr bool kEpi = kMode != kPlain, kKeepZ = kMode == kForwardZ,
+                        kTmaRes = kMode == kForwardResidual;
   using Params = DensePairParams;
   struct Tile {
     int j0, m0;
   };
-  static constexpr uint32_t kEpiSmemBytes = kStoreBoxes * kStoreBoxBytes;
+  // Two groups of four epilogue warps take the tile's 64-column boxes in turn,
+  // each with a store box of its own (two with Z or a residual): a tile of
+  // K = 1024 takes 6 us of MMAs, and one group of four took 13 us over its GELU,
+  // bias loads and stores.
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kMaxRegs = 200;  // 320 threads
+  static constexpr uint32_t kGroupBytes = (kKeepZ || kTmaRes ? 2 : 1) * kStoreBoxBytes;
+  static constexpr uint32_t kEpiSmemBytes = 2 * kGroupBytes + (kTmaRes ? 64 : 0);
 
   static __device__ __forceinline__ void prefetch(const Params& p) {
     tma_prefetch_desc(&p.tmRow);
@@ -84,89 +112,127 @@ struct DensePairPolicy {
     return kColMn ? mnmajor_desc(b, ks) : kmajor_desc(b, ks);
   }
 
-  // Sixty-four values of this thread's row as bf16 into the next store box and
-  // out: as store_box_bf16, from registers.
-  static __device__ __forceinline__ void emit(const float (&v)[64], const CUtensorMap* tm, int x,
-                                              int y, EpiCtx& e) {
-    const uint32_t buf = e.counter % kStoreBoxes;
-    ++e.counter;
-    if (e.tid == 0) tma_store_wait_read<kStoreBoxes - 1>();
-    named_bar_sync(1, 128);
-    uint8_t* sbuf = e.smem + buf * kStoreBoxBytes;
+  // 16 values of this thread's row as the 16-byte chunks c, c + 1 of a 64-column
+  // store box (128-byte swizzle)
+  static __device__ __forceinline__ void put2(uint8_t* box, int row, int c, const float (&v)[16]) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint4 q;
-      q.x = pack_bf16x2(v[8 * c], v[8 * c + 1]);
-      q.y = pack_bf16x2(v[8 * c + 2], v[8 * c + 3]);
-      q.z = pack_bf16x2(v[8 * c + 4], v[8 * c + 5]);
-      q.w = pack_bf16x2(v[8 * c + 6], v[8 * c + 7]);
-      *reinterpret_cast<uint4*>(sbuf + e.row * 128 + ((c ^ (e.row & 7)) * 16)) = q;
-    }
-    fence_async_shared();
-    named_bar_sync(1, 128);
-    if (e.tid == 0) {
-      tma_store_2d(tm, e.smem_u32 + buf * kStoreBoxBytes, x, y);
-      tma_store_commit();
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint4*>(box + row * 128 + (((c + h) ^ (row & 7)) * 16)) = pack8(v + 8 * h);
+  }
+  // A half box's residual: 8 columns per load, all inside or all beyond M.
+  struct Residual {
+    uint4 q[4];
+  };
+  static __device__ __forceinline__ void fetch(const Params& p, int row, int x, Residual& r) {
+    const size_t at = static_cast<size_t>(row) * p.M + x;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      r.q[c] = make_uint4(0, 0, 0, 0);
+      if (x + c * 8 < p.M && row < p.J &&
+          in_bounds(p.c.status, at + c * 8, 8, static_cast<size_t>(p.J) * p.M))
+        r.q[c] = *reinterpret_cast<const uint4*>(p.residual + at + c * 8);
     }
   }
-  static __device__ __forceinline__ void add8(float* v, const uint4& q) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] += __uint_as_float(w[j] << 16);
-      v[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
+  // Half boxes of 32 columns, one at a time (straight-line code for a whole box
+  // outgrows the instruction cache), the next one's residual in flight.
   static __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, uint32_t tacc,
                                                   EpiCtx& e) {
-    const int y0 = t.j0 + 128 * e.rank;
-    if constexpr (!kEpi) {
-      for (int bx = 0; bx < p.bn / 64 && t.m0 + bx * 64 < p.M; ++bx)
-        store_box_bf16(tacc, bx * 64, &p.tmOut, t.m0 + bx * 64, y0, e);
-    } else {
-      with_act(p.act, [&](auto tag) { boxes<decltype(tag)::value>(p, t, tacc, e, y0); });
+    const int y0 = t.j0 + 128 * e.rank, row = y0 + e.row;
+    const int nbox = min(p.bn, p.M - t.m0 + 63) / 64;
+    uint8_t* const box = e.smem + e.group * kGroupBytes;
+    const uint32_t box_u32 = e.smem_u32 + e.group * kGroupBytes;
+    const int bar = 1 + e.group;
+    Residual next;
+    const bool has_r = kKeepZ && p.residual != nullptr;
+    if (has_r && e.group < nbox) fetch(p, row, t.m0 + e.group * 64, next);
+    // kTmaRes: the group's boxes alternate between its two buffers; a box's
+    // residual is on its way while the box before it is finished. The buffers'
+    // barriers are made at the group's first box.
+    const uint32_t rbar = e.smem_u32 + 2 * kGroupBytes + e.group * 16u;
+    auto load_residual = [&](int b, uint32_t n) {  // thread 0: box b as the group's n-th
+      tma_store_wait_read<0>();                    // the buffer's last store has been read
+      mbar_arrive_expect_tx(rbar + 8u * (n & 1), kStoreBoxBytes);
+      tma_load_2d(box_u32 + (n & 1) * kStoreBoxBytes, &p.tmZ, rbar + 8u * (n & 1), t.m0 + b * 64,
+                  y0);
+    };
+    if (kTmaRes && e.tid == 0 && e.group < nbox) {
+      if (e.counter == 0) {
+        mbar_init(rbar, 1);
+        mbar_init(rbar + 8u, 1);
+        fence_barrier_init();
+      }
+      load_residual(e.group, e.counter);
     }
-  }
-  template <int ACT>
-  static __device__ __forceinline__ void boxes(const Params& p, const Tile& t, uint32_t tacc,
-                                               EpiCtx& e, int y0) {
-    const int row = y0 + e.row;
-    for (int bx = 0; bx < p.bn / 64; ++bx) {
-      const int x = t.m0 + bx * 64;
-      if (x >= p.M) break;
-      // the row's residual and the bias first: their latency passes during the
-      // loads from tensor memory (8 columns per load, all inside or all beyond M)
-      uint4 rq[8], bq[8];
+    if (kTmaRes && e.counter == 0) named_bar_sync(bar, 128);  // the barriers exist
+#pragma unroll 1
+    for (int i = 2 * e.group; i < 2 * nbox; i += (i & 1) ? 3 : 1) {
+      const int half = i & 1, col = i * 32, x = t.m0 + (i >> 1) * 64;
+      uint8_t* const dst = box + (kTmaRes ? (e.counter & 1) * kStoreBoxBytes : 0u);
+      __syncwarp();
+      uint32_t raw[32];
+      tmem_ld_32x32b_x32(tacc + col, raw);
+      uint4 bq[4];
+      if (kEpi && p.bias) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const bool in = x + c * 8 < p.M;
-        const size_t at = static_cast<size_t>(row) * p.M + x + c * 8;
-        rq[c] = make_uint4(0, 0, 0, 0);
-        if (p.residual && in && row < p.J &&
-            in_bounds(p.c.status, at, 8, static_cast<size_t>(p.J) * p.M))
-          rq[c] = *reinterpret_cast<const uint4*>(p.residual + at);
-        bq[c] = p.bias && in ? __ldg(reinterpret_cast<const uint4*>(p.bias + x + c * 8))
-                             : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c)
+          bq[c] = t.m0 + col + c * 8 < p.M
+                      ? __ldg(reinterpret_cast<const uint4*>(p.bias + t.m0 + col + c * 8))
+                      : make_uint4(0, 0, 0, 0);
       }
-      uint32_t raw[2][32];
-      tmem_ld_32x32b_x32(tacc + bx * 64, raw[0]);
-      tmem_ld_32x32b_x32(tacc + bx * 64 + 32, raw[1]);
+      const Residual r = next;
+      const int ni = i + (half ? 3 : 1);
+      if (has_r && ni < 2 * nbox) fetch(p, row, t.m0 + ni * 32, next);
+      if (kTmaRes && !half) {
+        if (e.tid == 0 && (i >> 1) + 2 < nbox) load_residual((i >> 1) + 2, e.counter + 1);
+        if (!mbar_wait_until(rbar + 8u * (e.counter & 1), (e.counter >> 1) & 1,
+                             globaltimer_ns() + kWaitLimitNs))
+          atomicOr(p.c.status, kStatusTimeout);
+      }
       tmem_ld_wait();
-      float v[64];
-#pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = f32(raw[i / 32][i % 32]);
-      if (p.bias) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) add8(v + 8 * c, bq[c]);
+      if (!kTmaRes && !half) {  // the box is free once its last store has been read
+        if (e.tid == 0) tma_store_wait_read<0>();
+        named_bar_sync(bar, 128);
       }
-      if (p.keep_z) emit(v, &p.tmZ, x, y0, e);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = act_f<ACT, true>(v[i]);
-      if (p.residual) {
+      for (int c = 0; c < 4; c += 2) {
+        float v[16];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) add8(v + 8 * c, rq[c]);
+        for (int j = 0; j < 16; ++j) v[j] = f32(raw[8 * c + j]);
+        if (kEpi) {
+          if (p.bias) {
+            add8(v, bq[c]);
+            add8(v + 8, bq[c + 1]);
+          }
+          if (kKeepZ) put2(box + kStoreBoxBytes, e.row, half * 4 + c, v);
+          // the branch on the activation sits here: around the whole loop it
+          // costs the registers of five loops
+          with_act(p.act, [&](auto tag) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = act_f<decltype(tag)::value, true>(v[j]);
+          });
+          if (kTmaRes) {  // the residual's chunks lie where the result's will
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              add8(v + 8 * h, *reinterpret_cast<const uint4*>(
+                                  dst + e.row * 128 + (((half * 4 + c + h) ^ (e.row & 7)) * 16)));
+          }
+          if (has_r) {
+            add8(v, r.q[c]);
+            add8(v + 8, r.q[c + 1]);
+          }
+        }
+        put2(dst, e.row, half * 4 + c, v);
       }
-      emit(v, &p.tmOut, x, y0, e);
+      if (half) {
+        fence_async_shared();
+        named_bar_sync(bar, 128);
+        if (e.tid == 0) {
+          tma_store_2d(&p.tmOut, box_u32 + static_cast<uint32_t>(dst - box), x, y0);
+          if (kKeepZ) tma_store_2d(&p.tmZ, box_u32 + kStoreBoxBytes, x, y0);
+          tma_store_commit();
+        }
+        ++e.counter;
+      }
     }
   }
   static __device__ __forceinline__ void epilogue_drain(const Params&, EpiCtx& e) { store_drain(e); }
@@ -181,9 +247,9 @@ bool encode_2d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, uin
   return encode_tmap_bf16(tm, base, 2, dims, strides, box, 128);
 }
 
-template <bool kRowMn, bool kColMn, bool kEpi>
+template <bool kRowMn, bool kColMn, PairEpilogue kMode>
 int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  using Pol = DensePairPolicy<kRowMn, kColMn, kEpi>;
+  using Pol = DensePairPolicy<kRowMn, kColMn, kMode>;
   DensePairParams p;
   p.J = static_cast<int>(g.J);
   p.M = static_cast<int>(g.M);
@@ -191,7 +257,6 @@ int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool
   p.bn = g.M > 128 ? 256 : 128;
   p.tiles_m = ceil_div(g.M, p.bn);
   p.act = g.act;
-  p.keep_z = g.Z != nullptr ? 1 : 0;
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
   p.residual = static_cast<const __nv_bfloat16*>(g.residual);
   // the row operand is B of the product (rows j), the column operand A (m)
@@ -200,7 +265,8 @@ int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool
       (kColMn ? encode_2d(&p.tmCol, g.A, g.M, g.K, 64)
               : encode_2d(&p.tmCol, g.A, g.K, g.M, static_cast<uint32_t>(p.bn / 2))) &&
       encode_2d(&p.tmOut, g.Out, g.M, g.J, 128) &&
-      encode_2d(&p.tmZ, g.Z ? g.Z : g.Out, g.M, g.J, 128);
+      encode_2d(&p.tmZ, kMode == kForwardZ ? g.Z : kMode == kForwardResidual ? g.residual : g.Out,
+                g.M, g.J, 128);
   if (!ok) return -2;
   const int64_t tiles = static_cast<int64_t>(ceil_div(g.J, 256)) * p.tiles_m;
   if (tiles > 0x7fffffff) return -2;
@@ -212,11 +278,11 @@ int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool
   return launch_gemm_pair<Pol>(p, smem, dev, s, pdl);
 }
 
-// ---------------------------------------------------------------- streams ----
-// The same products where the 256 x 256 tiles are few (stream_gemm.cuh): a tile
-// is 128 columns m of the output (A's rows) x nb rows j, so a thread holds one m
-// and a warp's stores of one j are 64 contiguous bytes.
-struct DenseStreamParams {
+// --------------------------------------------------------------- clusters ----
+// The same products where the 256 x 256 tiles are few or mostly empty
+// (split_kernel of stream_gemm.cuh): a tile is 128 columns m of the output (A's
+// rows) x nb rows j, its steps shared by a cluster of cs CTAs.
+struct DenseSplitParams {
   StreamCommon c;
   CUtensorMap tmA, tmB;
   int M, J, K, tiles_j;
@@ -228,9 +294,8 @@ struct DenseStreamParams {
 };
 
 template <bool kAMn, bool kBMn, bool kEpi>
-struct DenseStreamPolicy {
-  using Params = DenseStreamParams;
-  struct Acc {};
+struct DenseSplitPolicy {
+  using Params = DenseSplitParams;
   static constexpr uint32_t kSmemBytes = 0;
   static constexpr uint64_t kAStep = kAMn ? 128 : 2, kBStep = kBMn ? 128 : 2;
 
@@ -238,13 +303,7 @@ struct DenseStreamPolicy {
     tma_prefetch_desc(&p.tmA);
     tma_prefetch_desc(&p.tmB);
   }
-  static __device__ __forceinline__ void setup(const Params&, uint8_t*) {}
-  static __device__ __forceinline__ void shape(const Params& p, uint8_t*, int& tiles, int& nsub,
-                                               int& ks) {
-    tiles = ceil_div_dev(p.M, 128) * p.tiles_j;
-    nsub = 1;
-    ks = ceil_div_dev(p.K, 64);
-  }
+  static __device__ __forceinline__ int steps(const Params& p) { return ceil_div_dev(p.K, 64); }
   // tiles of the same rows of A are neighbours: they share A through L2
   static __device__ __forceinline__ int m_of(const Params& p, int tile) {
     return tile / p.tiles_j * 128;
@@ -252,8 +311,8 @@ struct DenseStreamPolicy {
   static __device__ __forceinline__ int j_of(const Params& p, int tile) {
     return tile % p.tiles_j * p.c.nb;
   }
-  static __device__ __forceinline__ void load_a(const Params& p, uint8_t*, int tile, int, int k,
-                                                uint32_t dst, uint32_t bar) {
+  static __device__ __forceinline__ void load_a(const Params& p, int tile, int k, uint32_t dst,
+                                                uint32_t bar) {
     const int m = m_of(p, tile);
     if (kAMn) {
       tma_load_2d(dst, &p.tmA, bar, m, k * 64);
@@ -262,8 +321,8 @@ struct DenseStreamPolicy {
       tma_load_2d(dst, &p.tmA, bar, k * 64, m);
     }
   }
-  static __device__ __forceinline__ void load_b(const Params& p, uint8_t*, int tile, int, int k,
-                                                uint32_t dst, uint32_t bar) {
+  static __device__ __forceinline__ void load_b(const Params& p, int tile, int k, uint32_t dst,
+                                                uint32_t bar) {
     const int j = j_of(p, tile);
     if (kBMn) {
       for (int q = 0; q < p.c.nb; q += 64)
@@ -278,83 +337,43 @@ struct DenseStreamPolicy {
   static __device__ __forceinline__ uint64_t bdesc(uint32_t b) {
     return kBMn ? mnmajor_desc(b, 0) : kmajor_desc(b, 0);
   }
-  // Columns col0 .. col0 + n - 1 of the tile, this thread's row: out.
-  template <int ACT>
-  static __device__ __forceinline__ void finish(const Params& p, int j0, int m, float bias,
-                                                const float (&v)[32], int n) {
-    if (m >= p.M) return;
-    const size_t extent = static_cast<size_t>(p.J) * p.M;
-    float r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const size_t at = static_cast<size_t>(j0 + i) * p.M + m;
-      r[i] = kEpi && p.residual && i < n && in_bounds(p.c.status, at, 1, extent)
-                 ? __bfloat162float(p.residual[at])
-                 : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i >= n) break;
-      const size_t at = static_cast<size_t>(j0 + i) * p.M + m;
-      if (!in_bounds(p.c.status, at, 1, extent)) continue;
-      const float z = v[i] + bias;
-      if (kEpi && p.Z) p.Z[at] = __float2bfloat16_rn(z);
-      p.Out[at] = __float2bfloat16_rn(act_f<ACT, true>(z) + r[i]);
-    }
+  static __device__ __forceinline__ int columns(const Params& p, int tile) {
+    return min(p.c.nb, p.J - j_of(p, tile));
   }
-  template <class Release>
-  static __device__ __forceinline__ void segment(const Params& p, uint8_t*, const StreamSeg& s,
-                                                 int per_tile, uint32_t tacc, StreamEpi& e, Acc&,
-                                                 const Release& release) {
-    const int j0 = j_of(p, s.tile), m = m_of(p, s.tile) + e.row;
-    const int n = min(p.c.nb, p.J - j0);
-    const float bias = kEpi && p.bias && m < p.M ? __bfloat162float(p.bias[m]) : 0.f;
-    auto out = [&](const float(&v)[32], int col) {
-      if (kEpi)
-        with_act(p.act, [&](auto tag) {
-          finish<decltype(tag)::value>(p, j0 + col, m, bias, v, n - col);
-        });
-      else
-        finish<DYRA_ACT_NONE>(p, j0 + col, m, bias, v, n - col);
-    };
-    float* part = stream_part(p.c, static_cast<int>(blockIdx.x), s.first) + e.row;
-    for (int col = 0; col < n; col += 32) {
-      __syncwarp();
-      uint32_t raw[32];
-      tmem_ld_32x32b_x32(tacc + col, raw);
-      tmem_ld_wait();
-      float v[32];
+  static __device__ __forceinline__ void finish8(const Params& p, int tile, int octet, int col,
+                                                 float (&v)[8]) {
+    const int j = j_of(p, tile) + col, m = m_of(p, tile) + octet * 8;
+    const size_t at = static_cast<size_t>(j) * p.M + m;
+    if (m >= p.M || !in_bounds(p.c.status, at, 8, static_cast<size_t>(p.J) * p.M)) return;
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (kEpi) {
+      if (p.residual) r = *reinterpret_cast<const uint4*>(p.residual + at);
+      if (p.bias) add8(v, __ldg(reinterpret_cast<const uint4*>(p.bias + m)));
+      if (p.Z) *reinterpret_cast<uint4*>(p.Z + at) = pack8(v);
+      with_act(p.act, [&](auto tag) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = f32(raw[i]);
-      if (s.whole) {
-        out(v, col);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (col + i < n) part[(col + i) * 128] = v[i];
-      }
+        for (int i = 0; i < 8; ++i) v[i] = act_f<decltype(tag)::value, true>(v[i]);
+      });
+      if (p.residual) add8(v, r);
     }
-    release();
-    if (s.whole) return;
-    int c0, c1;
-    if (!stream_arrive(p.c, s, per_tile, e, c0, c1)) return;
-    for (int col = 0; col < n; col += 32) {
-      float v[32];
-      stream_sum(p.c, c0, c1, e.row, col, n - col, v);
-      out(v, col);
-    }
+    *reinterpret_cast<uint4*>(p.Out + at) = pack8(v);
   }
-  static __device__ __forceinline__ void nothing(const Params&, const StreamEpi&) {}
+};
+
+struct SplitChoice {
+  int nb = 0;  // columns of a tile; 0: CTA pairs
+  int cs = 1;  // CTAs per tile
 };
 
 template <bool kAMn, bool kBMn, bool kEpi>
-int launch_stream(const LinearGemm& g, int nb, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  using Pol = DenseStreamPolicy<kAMn, kBMn, kEpi>;
-  DenseStreamParams p;
+int launch_split(const LinearGemm& g, SplitChoice ch, const DeviceInfo& dev, cudaStream_t s,
+                 bool pdl) {
+  using Pol = DenseSplitPolicy<kAMn, kBMn, kEpi>;
+  DenseSplitParams p;
   p.M = static_cast<int>(g.M);
   p.J = static_cast<int>(g.J);
   p.K = static_cast<int>(g.K);
-  p.tiles_j = ceil_div(g.J, nb);
+  p.tiles_j = ceil_div(g.J, ch.nb);
   p.act = g.act;
   p.bias = static_cast<const __nv_bfloat16*>(g.bias);
   p.residual = static_cast<const __nv_bfloat16*>(g.residual);
@@ -362,50 +381,80 @@ int launch_stream(const LinearGemm& g, int nb, const DeviceInfo& dev, cudaStream
   p.Z = static_cast<__nv_bfloat16*>(g.Z);
   if (!(kAMn ? encode_2d(&p.tmA, g.A, g.M, g.K, 64) : encode_2d(&p.tmA, g.A, g.K, g.M, 128)) ||
       !(kBMn ? encode_2d(&p.tmB, g.B, g.J, g.K, 64)
-             : encode_2d(&p.tmB, g.B, g.K, g.J, static_cast<uint32_t>(nb))))
+             : encode_2d(&p.tmB, g.B, g.K, g.J, static_cast<uint32_t>(ch.nb))))
     return -2;
   const uint32_t smem =
-      stream_setup<Pol>(p.c, nb, kAMn, kBMn, g.ws, g.counters, g.status, dev);
+      stream_setup<Pol>(p.c, ch.nb, kAMn, kBMn, nullptr, nullptr, g.status, dev);
   if (!smem) return -3;
-  return stream_launch<Pol>(p, smem, dev, s, pdl);
+  return split_launch<Pol>(p, ceil_div(g.M, 128) * p.tiles_j, ch.cs, smem, dev, s, pdl);
 }
 
-// Columns of a stream tile for the product, 0: the CTA pairs take it.
-int stream_columns(const LinearGemm& g, const DeviceInfo& dev) {
+// Clusters of cs CTAs (one CTA per SM) that run at once: a cluster stays within
+// a group of SMs, whose count no cluster size above 2 divides evenly.
+int resident_clusters(int cs, const DeviceInfo& dev) {
+  static std::atomic<int> known[kMaxDevices][9];
+  if (cs == 1) return dev.sm_count;
+  if (dev.device < 0 || dev.device >= kMaxDevices) return dev.sm_count / 8;
+  int n = known[dev.device][cs].load();
+  if (n == 0) {
+    n = split_resident<DenseSplitPolicy<false, false, true>>(cs, dev);
+    known[dev.device][cs].store(n);
+  }
+  return n;
+}
+
+// CTA pairs or clusters, by a model of both in nanoseconds, fitted to 4096 ->
+// 14336, 1280 -> 5120, 4096 -> 1024, 1024 -> 1024 and 1024 -> 4096 at 1 to 1024
+// rows (cold weights). A pair's step of 256 x 256 x 64 takes 350 whatever part of
+// the tile exists; a cluster CTA's step takes its 16 KB of A and nb rows of B at
+// 75 bytes per ns, and finishing a tile costs its columns. 64 rows through 1024 ->
+// 1024: 6.2 us in clusters of 4, 15.3 on pairs; 512 rows through 4096 -> 14336: 57
+// on pairs, 105 in clusters.
+SplitChoice choose_split(const LinearGemm& g, const DeviceInfo& dev) {
+  const int64_t ks = ceil_div(g.K, 64), tm = ceil_div(g.M, 128);
+  const double weights_ns = 2.0 * static_cast<double>(g.M) * g.K / 5200.0;
   const int64_t pair_tiles =
       static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
-  if (g.J > kStreamMaxNb && pair_tiles > dev.sm_count / 2) return 0;
-  const int tj = ceil_div(g.J, kStreamMaxNb);
-  int nb = ceil_div(ceil_div(g.J, tj), 16) * 16;
-  if (g.b_mn) nb = nb <= 64 ? 64 : 128;  // whole boxes of 64
-  // steps are counted in 32 bits
-  if (static_cast<double>(ceil_div(g.M, 128)) * ceil_div(g.J, nb) * ceil_div(g.K, 64) > 1e9)
-    return 0;
-  return nb;
+  const int64_t pairs = dev.sm_count / 2;
+  SplitChoice best;
+  double best_ns = 6500.0 + static_cast<double>((pair_tiles + pairs - 1) / pairs) *
+                                (350.0 * static_cast<double>(ks) + 2000.0);
+  if (pair_tiles > 2 * pairs) return best;  // many full tiles
+  const int exact = ceil_div(std::min<int64_t>(g.J, kStreamMaxNb), 16) * 16;
+  for (int nb : {16, 32, 64, exact, kStreamMaxNb}) {
+    if (nb > exact && !(g.b_mn && nb == 64)) continue;
+    if (g.b_mn && nb % 64) continue;  // whole boxes of 64
+    const int64_t tiles = tm * ceil_div(g.J, nb);
+    if (tiles > 4 * dev.sm_count) continue;
+    for (int cs = 1; cs <= 8 && cs <= ks; ++cs) {
+      const int64_t waves = (tiles + resident_clusters(cs, dev) - 1) / resident_clusters(cs, dev);
+      const double cta_ns = static_cast<double>(ceil_div(ks, cs)) * (16384 + 128 * nb) / 75.0 +
+                            30.0 * nb / cs + 10.0 * nb + 100.0 * cs;
+      const double ns = 4500.0 + std::max(static_cast<double>(waves) * cta_ns, weights_ns);
+      if (ns < best_ns) {
+        best_ns = ns;
+        best.nb = nb;
+        best.cs = cs;
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
-size_t linear_ws_bytes(const DeviceInfo& dev) {
-  return static_cast<size_t>(dev.sm_count) * 2 * kStreamMaxNb * 128 * sizeof(float);
-}
-
-// Tiles of a stream: one per 128 columns m of up to kStreamMaxNb rows, or where
-// the pairs' tiles are at most half the SMs, four of 128 x 128 for each of those.
-int linear_counters(int d_in, int d_out, const DeviceInfo& dev) {
-  return std::max(ceil_div(std::max(d_in, d_out), 128), dev.sm_count / 2 * 4);
-}
-
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  const int nb = stream_columns(g, dev);
+  const SplitChoice ch = choose_split(g, dev);
   if (g.a_mn && g.b_mn)
-    return nb ? launch_stream<true, true, false>(g, nb, dev, s, pdl)
-              : launch_pair<true, true, false>(g, dev, s, pdl);
+    return ch.nb ? launch_split<true, true, false>(g, ch, dev, s, pdl)
+                 : launch_pair<true, true, kPlain>(g, dev, s, pdl);
   if (g.a_mn)
-    return nb ? launch_stream<true, false, false>(g, nb, dev, s, pdl)
-              : launch_pair<false, true, false>(g, dev, s, pdl);
-  return nb ? launch_stream<false, false, true>(g, nb, dev, s, pdl)
-            : launch_pair<false, false, true>(g, dev, s, pdl);
+    return ch.nb ? launch_split<true, false, false>(g, ch, dev, s, pdl)
+                 : launch_pair<false, true, kPlain>(g, dev, s, pdl);
+  if (ch.nb) return launch_split<false, false, true>(g, ch, dev, s, pdl);
+  if (g.Z) return launch_pair<false, false, kForwardZ>(g, dev, s, pdl);
+  return g.residual ? launch_pair<false, false, kForwardResidual>(g, dev, s, pdl)
+                    : launch_pair<false, false, kForward>(g, dev, s, pdl);
 }
 
 }  // namespace dyra

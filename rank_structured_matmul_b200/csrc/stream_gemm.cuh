@@ -333,6 +333,173 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
 }
 
+// The same product with each tile on a cluster of its own: the cluster's CTAs
+// take equal shares of the tile's steps, leave their fp32 parts in their shared
+// memory (the operand stages, free by then) and each sums and finishes a share of
+// the columns over all parts, in CTA order, through distributed shared memory.
+// Where a tile needs several CTAs and has many columns this is the cheaper way to
+// join them: the parts of 64 columns from 16 CTAs took one CTA of the kernel
+// above 45 us to sum. One tile per cluster, at most as many CTAs as steps. Of a
+// policy it takes prefetch, adesc, bdesc, kAStep and kBStep as above, and
+//   static int steps(p);
+//   static void load_a / load_b(p, tile, k, dst, bar);
+//   static int columns(p, tile);  // of the tile that exist
+//   static void finish8(p, tile, octet, col, float (&v)[8]);  // rows 8 octet ..
+template <class Pol>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    split_kernel(const __grid_constant__ typename Pol::Params p, int cs) {
+  extern __shared__ uint8_t smem_raw[];
+  const StreamCommon& c = p.c;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sbase = raw + pad;
+  const int S = c.stages;
+  const uint32_t sA = sbase, sB = sA + static_cast<uint32_t>(S) * kStreamABytes;
+  const uint32_t off_bar = static_cast<uint32_t>(S) * (kStreamABytes + c.b_bytes);
+  const uint32_t sBar = sbase + off_bar;
+  auto full_bar = [&](int s) { return sBar + 8u * s; };
+  auto empty_bar = [&](int s) { return sBar + 8u * (kStreamMaxStages + s); };
+  const uint32_t done_bar = sBar + 8u * (2 * kStreamMaxStages);
+  uint32_t* words = reinterpret_cast<uint32_t*>(smem + off_bar + 8 * (2 * kStreamMaxStages + 1));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / cs;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) Pol::prefetch(p);
+  if (warp == 1) {
+    tmem_alloc(smem_u32(words), c.tmem_cols);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = words[0];
+  const int ks = Pol::steps(p);
+  const int k0 = static_cast<int>(static_cast<long long>(rank) * ks / cs);
+  const int k1 = static_cast<int>(static_cast<long long>(rank + 1) * ks / cs);
+  WaitCtx w{abort_flag, c.status, c.wait_ns};
+  uint32_t last_phase[kStreamMaxStages];
+  uint32_t issued = 0;
+
+  if (warp == 0) {
+    if (elect_one_sync()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int k = k0; k < k1; ++k) {
+        if (!mbar_wait(empty_bar(stage), phase ^ 1u, w)) break;
+        mbar_arrive_expect_tx(full_bar(stage), kStreamABytes + c.b_bytes);
+        Pol::load_a(p, tile, k, sA + stage * kStreamABytes, full_bar(stage));
+        Pol::load_b(p, tile, k, sB + stage * c.b_bytes, full_bar(stage));
+        issued |= 1u << stage;
+        last_phase[stage] = phase;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (elect_one_sync()) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int k = k0; k < k1; ++k) {
+        const uint64_t a0 = Pol::adesc(sA + stage * kStreamABytes);
+        const uint64_t b0 = Pol::bdesc(sB + stage * c.b_bytes);
+        if (!mbar_wait(full_bar(stage), phase, w)) break;
+        tc_fence_after();
+        issue_stage<false>(tmem, a0, Pol::kAStep, b0, Pol::kBStep, c.idesc, 4, k == k0);
+        mma_commit(empty_bar(stage));
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      mma_commit(done_bar);
+      (void)mbar_wait_until(done_bar, 0, globaltimer_ns() + kWaitLimitNs);
+    }
+  } else {
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const bool good = stream_all(mbar_wait(done_bar, 0, w));
+    tc_fence_after();
+    const int n = Pol::columns(p, tile);
+    const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    float* part = reinterpret_cast<float*>(smem);  // [column][128 rows]
+    for (int col = 0; good && col < n; col += 32) {
+      __syncwarp();
+      uint32_t r[32];
+      tmem_ld_32x32b_x32(tacc + col, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < n) part[(col + i) * 128 + row] = f32(r[i]);
+    }
+  }
+  // every part is in place
+  __syncwarp();
+  if (cs > 1)
+    cluster_sync_all();
+  else
+    block_sync_all();
+  if (!*abort_flag) {
+    // eight rows of one column at a time: 16-byte pieces of the output, a
+    // column's sixteen on consecutive lanes
+    const int n = Pol::columns(p, tile);
+    const int c0 = rank * n / cs, c1 = (rank + 1) * n / cs;
+    constexpr int kFlight = 2;  // pieces of a thread in flight
+    for (int i0 = c0 * 16 + static_cast<int>(threadIdx.x); i0 < c1 * 16;
+         i0 += kFlight * kStreamThreads) {
+      float v[kFlight][8] = {};
+      for (int q = 0; q < cs; ++q) {
+        float4 x[kFlight][2];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          // beyond the share: the first piece again, unused
+          const int i = i0 + u * kStreamThreads < c1 * 16 ? i0 + u * kStreamThreads : i0;
+          const uint32_t at = sbase + static_cast<uint32_t>(i) * 32u;  // [column][octet][8]
+          const uint32_t from = cs > 1 ? mapa_shared(at, static_cast<uint32_t>(q)) : at;
+          x[u][0] = ld_shared_cluster_v4(from);
+          x[u][1] = ld_shared_cluster_v4(from + 16u);
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+          v[u][0] += x[u][0].x, v[u][1] += x[u][0].y, v[u][2] += x[u][0].z, v[u][3] += x[u][0].w;
+          v[u][4] += x[u][1].x, v[u][5] += x[u][1].y, v[u][6] += x[u][1].z, v[u][7] += x[u][1].w;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int i = i0 + u * kStreamThreads;
+        if (i < c1 * 16) Pol::finish8(p, tile, i & 15, i >> 4, v[u]);
+      }
+    }
+  }
+  __syncwarp();
+  if (cs > 1) cluster_sync_all();  // no CTA leaves while its part is read
+  block_sync_all();
+  if (warp == 0 && issued && *abort_flag) {
+    const unsigned long long deadline = globaltimer_ns() + kWaitLimitNs;
+    for (int s = 0; s < S; ++s)
+      if (issued & (1u << s)) (void)mbar_wait_until(full_bar(s), last_phase[s], deadline);
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, c.tmem_cols);
+  }
+}
+
 // Fill the shared launch parameters for nb columns; the dynamic shared memory
 // of a block, or 0 if it does not fit.
 template <class Pol>
@@ -356,21 +523,27 @@ uint32_t stream_setup(StreamCommon& c, int nb, bool a_mn, bool b_mn, float* ws, 
   return stream_smem_bytes(c.stages, c.b_bytes, Pol::kSmemBytes);
 }
 
+// Dynamic shared memory limits of the kernel raised to `smem` bytes.
+template <class Kernel>
+int raise_smem(Kernel kfn, KernelSetup& setup, uint32_t smem, const DeviceInfo& dev) {
+  const int d = dev.device;
+  if (d < 0 || d >= kMaxDevices) return -1;
+  if (smem <= setup.smem[d].load()) return 0;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
+          cudaSuccess)
+    return -1;
+  setup.smem[d].store(smem);
+  return 0;
+}
+
 template <class Pol>
 int stream_launch(const typename Pol::Params& p, uint32_t smem, const DeviceInfo& dev,
                   cudaStream_t s, bool pdl) {
   auto kfn = stream_kernel<Pol>;
   static KernelSetup setup;
-  const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
-  if (smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-            cudaSuccess)
-      return -1;
-    setup.smem[d].store(smem);
-  }
+  if (raise_smem(kfn, setup, smem, dev)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count));
   cfg.blockDim = dim3(kStreamThreads);
@@ -382,6 +555,59 @@ int stream_launch(const typename Pol::Params& p, uint32_t smem, const DeviceInfo
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kfn, p) == cudaSuccess ? 0 : -1;
+}
+
+// Clusters of cs CTAs that can be resident at once, at a CTA per SM.
+template <class Pol>
+int split_resident(int cs, const DeviceInfo& dev) {
+  static KernelSetup setup;
+  auto kfn = split_kernel<Pol>;
+  const uint32_t smem = static_cast<uint32_t>(dev.max_smem_optin);
+  int n = 0;
+  if (raise_smem(kfn, setup, smem, dev) == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cs * cs));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kfn, &cfg) != cudaSuccess) n = 0;
+  }
+  cudaGetLastError();
+  return n > 0 ? n : std::max(1, dev.sm_count / (2 * cs));
+}
+
+template <class Pol>
+int split_launch(const typename Pol::Params& p, int tiles, int cs, uint32_t smem,
+                 const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+  auto kfn = split_kernel<Pol>;
+  static KernelSetup setup;
+  if (raise_smem(kfn, setup, smem, dev)) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (pdl) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cs > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = static_cast<unsigned>(cs);
+    attr[na].val.clusterDim.y = 1;
+    attr[na++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = static_cast<unsigned>(na);
+  return cudaLaunchKernelEx(&cfg, kfn, p, cs) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace dyra

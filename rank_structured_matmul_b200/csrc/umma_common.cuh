@@ -220,7 +220,7 @@ int launch_gemm_pair(const typename Pol::Params& p, uint32_t smem, const DeviceI
   const int d = dev.device;
   if (d < 0 || d >= kMaxDevices) return -1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(64 + 32 * EpiWarps<Pol>::value);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   if (smem > setup.smem[d].load() || setup.occupancy[d].load() < 1) {

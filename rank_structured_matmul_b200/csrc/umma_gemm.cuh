@@ -125,7 +125,8 @@ struct EpiCtx {
   int row;            // tile row owned by this thread, 0..127
   int lane;           // lane in warp
   int quad;           // TMEM lane quadrant of this warp
-  int tid;            // 0..127 among the epilogue threads
+  int tid;            // 0..127 among the epilogue threads (of the group)
+  int group;          // group of four epilogue warps (0 unless EpiWarps is 8)
   uint8_t* smem;      // policy scratch (kEpiSmemBytes), 1024-byte aligned
   uint32_t smem_u32;  // same, as a shared-window address
   uint32_t counter;   // running counter the policy may use (e.g. store buffers)
@@ -152,6 +153,17 @@ struct MaxRegs {
 template <class Pol>
 struct MaxRegs<Pol, std::void_t<decltype(Pol::kMaxRegs)>> {
   static constexpr int value = Pol::kMaxRegs;
+};
+
+// Epilogue warps of a policy's pair kernel: Pol::kEpiWarps (4 or 8) if it
+// declares them, else 4. Eight are two groups of four, each over all 128 rows.
+template <class Pol, class = void>
+struct EpiWarps {
+  static constexpr int value = 4;
+};
+template <class Pol>
+struct EpiWarps<Pol, std::void_t<decltype(Pol::kEpiWarps)>> {
+  static constexpr int value = Pol::kEpiWarps;
 };
 
 // Whether a policy can split its first stages' copies around the dependency
@@ -402,6 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __maxnreg__(MaxRegs<Pol>::val
     e.lane = lane;
     e.row = e.quad * 32 + lane;
     e.tid = threadIdx.x - 64;
+    e.group = 0;
     e.smem = smem + (sEpi - sbase);
     e.smem_u32 = sEpi;
     e.counter = 0;

@@ -10,8 +10,8 @@
 //    only the leader arms it with the pair's byte count;
 //  - only the leader's warp 1 issues MMAs; completions are committed to the
 //    matching barrier of both CTAs (slot free, accumulator ready);
-//  - both CTAs' epilogue warps (8) arrive on the leader's accumulator-free
-//    barrier;
+//  - both CTAs' epilogue warps (8, or 16 with EpiWarps 8) arrive on the
+//    leader's accumulator-free barrier;
 //  - TMEM is allocated and freed pairwise; the cluster synchronises after
 //    set-up and before teardown.
 // Waits are bounded as in the single-CTA skeleton.
@@ -26,7 +26,7 @@
 namespace dyra {
 
 template <class Pol>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * EpiWarps<Pol>::value, 1)
     __maxnreg__(MaxRegs<Pol>::value)
     umma_gemm_pair_kernel(const __grid_constant__ typename Pol::Params p) {
   using namespace sm100;
@@ -68,7 +68,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(tfull_bar(i), 1);
-      mbar_init(tempty_bar(i), 8);  // 4 epilogue warps in each CTA of the pair
+      mbar_init(tempty_bar(i), 2 * EpiWarps<Pol>::value);  // the pair's epilogue warps
     }
     mbar_init(fin_bar, 1);
     *abort_flag = 0;
@@ -220,7 +220,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     e.quad = warp & 3;
     e.lane = lane;
     e.row = e.quad * 32 + lane;
-    e.tid = threadIdx.x - 64;
+    e.tid = (threadIdx.x - 64) & 127;
+    e.group = (warp - 2) >> 2;
     e.smem = smem + (sEpi - sbase);
     e.smem_u32 = sEpi;
     e.counter = 0;
@@ -232,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const uint32_t acc_phase = (local >> 1) & 1;
       if (!mbar_wait(tfull_bar(acc), acc_phase, w)) break;
       tc_fence_after();
-      if (tr && e.tid == 0 && local == 0) tr[kTrEpiFirst] = globaltimer_ns();
+      if (tr && e.tid == 0 && e.group == 0 && local == 0) tr[kTrEpiFirst] = globaltimer_ns();
       typename Pol::Tile t;
       Pol::decode(p, tile, t);
       const uint32_t tacc = tmem + static_cast<uint32_t>(acc) * c.acc_cols +
@@ -241,11 +242,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(tempty_bar(acc));
-      if (tr && e.tid == 0 && local < kTrTileMma - kTrTileDone)
+      if (tr && e.tid == 0 && e.group == 0 && local < kTrTileMma - kTrTileDone)
         tr[kTrTileDone + local] = globaltimer_ns();
     }
     Pol::epilogue_drain(p, e);
-    if (tr && e.tid == 0) tr[kTrEpiDone] = globaltimer_ns();
+    if (tr && e.tid == 0 && e.group == 0) tr[kTrEpiDone] = globaltimer_ns();
   }
   // Warps 0 and 1 ran their roles on one elected lane: reconverge them
   // before the closing barrier (which counts threads, so it holds the block
