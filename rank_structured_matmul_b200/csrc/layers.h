@@ -56,9 +56,14 @@ struct MoeShape {
   int d, f, experts, top_k, act, renorm;
 };
 
+// The router, kRouteTokens tokens per launch. logits: moe_logit_bytes of scratch;
+// counters: moe_route_counters ints, zero before and after the call.
+constexpr int kRouteTokens = 1024;
+size_t moe_logit_bytes(const MoeShape& m);
+int moe_route_counters();
 template <typename T>
 int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float* weights,
-                     int64_t N, int* status, cudaStream_t s);
+                     int64_t N, double* logits, int* counters, cudaStream_t s);
 
 // CUDA-core experts for N <= kMoeTokens tokens. hidden: N * top_k x f values,
 // part: N * top_k x d floats.
@@ -72,7 +77,7 @@ int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const
 // as the sizes below. pdl: launched behind the router's grid.
 int moe_reached_max(const MoeShape& m);
 int moe_counters(const MoeShape& m);
-size_t moe_ws_bytes(const DeviceInfo& dev);
+size_t moe_ws_bytes(const MoeShape& m, const DeviceInfo& dev);
 int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int* ids,
                             const float* weights, const __nv_bfloat16* Wgu,
                             const __nv_bfloat16* Wd, const __nv_bfloat16* residual,

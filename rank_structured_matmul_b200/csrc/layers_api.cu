@@ -32,7 +32,8 @@ struct dyra_moe {
   bool simt = false;
   void* hidden = nullptr;  // the hidden values of one group of kMoeTokens tokens
   float* part = nullptr;   // CUDA cores: its slots' outputs; tensor cores: parts of split tiles
-  int* tiles = nullptr;    // tensor cores: the tiles' arrival counters, zero between calls
+  double* logits = nullptr;  // the router's
+  int* tiles = nullptr;    // arrival counters, zero between calls: the router's, then the tiles'
   int* status = nullptr;
   size_t bytes = 0;
   int n_tiles = 0;
@@ -117,6 +118,7 @@ void dense_free(dyra_dense* p) {
 void moe_free(dyra_moe* p) {
   give(p->hidden);
   give(p->part);
+  give(p->logits);
   give(p->tiles);
   give(p->status);
   delete p;
@@ -126,7 +128,7 @@ template <class T>
 int moe_route(const dyra_moe* p, const void* X, const void* Wr, int32_t* ids, float* weights,
               int64_t N, cudaStream_t s) {
   return launch_moe_route<T>(p->m, static_cast<const T*>(X), static_cast<const T*>(Wr), ids,
-                             weights, N, p->status, s);
+                             weights, N, p->logits, p->tiles, s);
 }
 
 template <class T>
@@ -138,8 +140,8 @@ int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
       return launch_moe_experts_umma(p->m, static_cast<const T*>(X), ids, weights,
                                      static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                      static_cast<const T*>(residual), static_cast<T*>(Y), n,
-                                     static_cast<T*>(p->hidden), p->part, p->tiles, p->status,
-                                     p->dev, s, pdl);
+                                     static_cast<T*>(p->hidden), p->part,
+                                     p->tiles + moe_route_counters(), p->status, p->dev, s, pdl);
   return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
@@ -324,12 +326,13 @@ int dyra_moe_create(dyra_moe_t* out, int d_model, int d_ff, int experts, int top
   const size_t slots = static_cast<size_t>(kMoeTokens) * top_k;
   const size_t hidden_rows =
       p->simt ? slots : static_cast<size_t>(kMoeTokens) * moe_reached_max(p->m);
-  const size_t part_bytes = p->simt ? slots * d_model * sizeof(float) : moe_ws_bytes(dev);
-  p->n_tiles = p->simt ? 0 : moe_counters(p->m);
+  const size_t part_bytes = p->simt ? slots * d_model * sizeof(float) : moe_ws_bytes(p->m, dev);
+  p->n_tiles = moe_route_counters() + (p->simt ? 0 : moe_counters(p->m));
   if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
       (rc = take(&p->hidden, hidden_rows * d_ff * elem_size(dtype), &p->bytes)) ||
       (rc = take(&p->part, part_bytes, &p->bytes)) ||
-      (!p->simt && (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes)))) {
+      (rc = take(&p->logits, moe_logit_bytes(p->m), &p->bytes)) ||
+      (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes))) {
     moe_free(p);
     return rc;
   }

@@ -1,5 +1,5 @@
 // layers_moe_umma.cu - bf16 experts for up to 64 tokens on tcgen05 tensor cores,
-// in two kernels of stream_gemm.cuh's form.
+// in two kernels of stream_gemm.cuh's form and one that joins their parts.
 //
 // The layer is bound by reading the weights of the experts its tokens reach, so
 // each is read once and meets all tokens of the call: the tokens are the N side
@@ -10,8 +10,12 @@
 //            expert e: tiles of 64 gate rows over the 64 up rows of the same f
 //   down     y[n][d] = sum over a of w(n, e) (Wd_e hidden[a][n])[d]: tiles of 128
 //            rows d whose steps run through the reached experts; the weights are
-//            applied in fp32 at the end of each expert's run, and the running sum
-//            of a tile stays in registers
+//            applied in fp32 at the end of each expert's run, the running sum of
+//            a CTA's share of a tile stays in registers
+//   join     the shares' sums, in order, and the residual
+// A few tiles hold all of down's steps, so each has many parts (10 of 64 columns
+// at 64 tokens over 128 experts of 2048 x 1024): summed by the last CTA to arrive
+// they took about 20 us, spread over a grid of their own 3.
 // The down kernel starts while the gate-up kernel drains: its weights do not
 // depend on it and are copied before the wait.
 #include <algorithm>
@@ -79,6 +83,7 @@ struct GateUpParams {
 
 struct GateUpPolicy {
   using Params = GateUpParams;
+  static constexpr bool kWholeTiles = true;
   struct Acc {};
   struct Smem {
     float up[kMoeTokens][64];
@@ -180,12 +185,18 @@ struct DownParams {
   CUtensorMap tmH;  // (f, N, reached experts), box (64, nb, 1), rows kMoeTokens apart
   MoeTables t;
   int d, f;
-  const __nv_bfloat16* residual;  // may be Y
-  __nv_bfloat16* Y;
+  int* meta;  // for the join: steps, CTAs, steps of a tile
 };
+
+// The part of a tile that a CTA leaves: along the sequence of shares either the
+// tile or the CTA or both go up by one from part to part, so their sum names it.
+__device__ __forceinline__ float* down_part(const StreamCommon& c, int cta, int tile) {
+  return c.ws + static_cast<size_t>(cta + tile) * static_cast<size_t>(c.nb) * 128;
+}
 
 struct DownPolicy {
   using Params = DownParams;
+  static constexpr bool kWholeTiles = false;
   struct Acc {  // the running sums of this thread's row, column by column
     float v[kMoeTokens];
     bool fresh = true;
@@ -230,25 +241,6 @@ struct DownPolicy {
   static __device__ __forceinline__ uint64_t adesc(uint32_t a) { return kmajor_desc(a, 0); }
   static __device__ __forceinline__ uint64_t bdesc(uint32_t b) { return kmajor_desc(b, 0); }
 
-  static __device__ __forceinline__ void finish(const Params& p, int m, int col,
-                                                const float (&v)[32]) {
-    if (m >= p.d) return;
-    const size_t extent = static_cast<size_t>(p.t.N) * p.d;
-    float r[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const size_t at = static_cast<size_t>(col + i) * p.d + m;
-      r[i] = p.residual && col + i < p.t.N && in_bounds(p.c.status, at, 1, extent)
-                 ? __bfloat162float(p.residual[at])
-                 : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (col + i >= p.t.N) break;
-      const size_t at = static_cast<size_t>(col + i) * p.d + m;
-      if (in_bounds(p.c.status, at, 1, extent)) p.Y[at] = __float2bfloat16_rn(v[i] + r[i]);
-    }
-  }
   template <class Release>
   static __device__ __forceinline__ void segment(const Params& p, uint8_t* sm, const StreamSeg& s,
                                                  int per_tile, uint32_t tacc, StreamEpi& e,
@@ -288,35 +280,76 @@ struct DownPolicy {
       }
     }
     release();
-    if (!s.last) return;
-    const int m = s.tile * 128 + e.row;
-    if (s.whole) {
-#pragma unroll
-      for (int half = 0; half < kMoeTokens / 32; ++half)
-        if (half * 32 < p.t.N)
-          finish(p, m, half * 32, reinterpret_cast<const float(&)[32]>(acc.v[half * 32]));
-      return;
+    if (blockIdx.x == 0 && e.tid == 0) {
+      p.meta[0] = e.total;
+      p.meta[1] = e.grid;
+      p.meta[2] = per_tile;
     }
-    float* part = stream_part(p.c, static_cast<int>(blockIdx.x), s.first) + e.row;
+    if (!s.last) return;
+    float* part = down_part(p.c, static_cast<int>(blockIdx.x), s.tile) + e.row;
 #pragma unroll
     for (int i = 0; i < kMoeTokens; ++i)
       if (i < p.t.N) part[i * 128] = acc.v[i];
-    int c0, c1;
-    if (!stream_arrive(p.c, s, per_tile, e, c0, c1)) return;
-    for (int col = 0; col < p.t.N; col += 32) {
-      float v[32];
-      stream_sum(p.c, c0, c1, e.row, col, p.t.N - col, v);
-      finish(p, m, col, v);
-    }
   }
-  // no token names an expert: Y is the residual, or zero
+  // no token names an expert
   static __device__ __forceinline__ void nothing(const Params& p, const StreamEpi& e) {
-    const size_t n = static_cast<size_t>(p.t.N) * p.d;
-    for (size_t i = static_cast<size_t>(blockIdx.x) * 128 + e.tid; i < n;
-         i += static_cast<size_t>(gridDim.x) * 128)
-      p.Y[i] = p.residual ? p.residual[i] : __float2bfloat16_rn(0.f);
+    if (blockIdx.x == 0 && e.tid == 0) p.meta[0] = 0;
   }
 };
+
+// ------------------------------------------------------------------- join ----
+// Y[n][8 o ..] = the sum, in the CTAs' order, of the down tile's parts of that
+// column, plus the residual: eight rows of a token per thread.
+__global__ void __launch_bounds__(128)
+    moe_join_kernel(const __grid_constant__ StreamCommon c, const int* meta,
+                    const __nv_bfloat16* residual, __nv_bfloat16* Y, int N, int d) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int octets = d / 8;
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i >= octets * N) return;
+  const int n = i / octets, o = i - n * octets;
+  const size_t at = static_cast<size_t>(n) * d + static_cast<size_t>(o) * 8;
+  if (!in_bounds(c.status, at, 8, static_cast<size_t>(N) * d)) return;
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (residual) r = *reinterpret_cast<const uint4*>(residual + at);
+  const int total = meta[0];
+  float v[8] = {};
+  if (total > 0) {
+    const int grid = meta[1], per_tile = meta[2], tile = o / 16;
+    const int c0 = stream_owner(tile * per_tile, total, grid);
+    const int c1 = stream_owner(tile * per_tile + per_tile - 1, total, grid);
+    const size_t off = static_cast<size_t>(n) * 128 + (o % 16) * 8;
+    constexpr int kFlight = 6;  // parts in flight
+    for (int q0 = c0; q0 <= c1; q0 += kFlight) {
+      float4 x[kFlight][2];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const int q = min(q0 + u, c1);
+        const float4* part = reinterpret_cast<const float4*>(down_part(c, q, tile) + off);
+        x[u][0] = __ldcg(part);
+        x[u][1] = __ldcg(part + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u)
+        if (q0 + u <= c1) {
+          v[0] += x[u][0].x, v[1] += x[u][0].y, v[2] += x[u][0].z, v[3] += x[u][0].w;
+          v[4] += x[u][1].x, v[5] += x[u][1].y, v[6] += x[u][1].z, v[7] += x[u][1].w;
+        }
+    }
+  }
+  if (residual) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] += __uint_as_float(w[j] << 16);
+      v[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+  *reinterpret_cast<uint4*>(Y + at) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7]));
+}
 
 bool encode_3d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, int64_t slabs,
                int64_t slab_rows, uint32_t box_rows) {
@@ -332,12 +365,13 @@ bool encode_3d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, int
 
 int moe_reached_max(const MoeShape& m) { return std::min(m.experts, kMoeTokens * m.top_k); }
 
-int moe_counters(const MoeShape& m) {
-  return moe_reached_max(m) * ceil_div(m.f, 64) + ceil_div(m.d, 128);
-}
+// the gate-up tiles' arrival counters, then the join's three words
+int moe_counters(const MoeShape& m) { return moe_reached_max(m) * ceil_div(m.f, 64) + 4; }
 
-size_t moe_ws_bytes(const DeviceInfo& dev) {
-  return static_cast<size_t>(dev.sm_count) * 2 * kMoeTokens * 128 * sizeof(float);
+// two parts per CTA of gate-up, or down's: one per CTA and tile border
+size_t moe_ws_bytes(const MoeShape& m, const DeviceInfo& dev) {
+  const size_t parts = static_cast<size_t>(dev.sm_count) + std::max(dev.sm_count, ceil_div(m.d, 128));
+  return parts * kMoeTokens * 128 * sizeof(float);
 }
 
 int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int* ids,
@@ -360,8 +394,7 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
   w.t = t;
   w.d = m.d;
   w.f = m.f;
-  w.residual = residual;
-  w.Y = Y;
+  w.meta = counters + moe_reached_max(m) * ceil_div(m.f, 64);
   if (!encode_3d(&g.tmW, Wgu, m.d, 2 * static_cast<int64_t>(m.f), m.experts,
                  2 * static_cast<int64_t>(m.f), 64) ||
       !encode_3d(&g.tmX, X, m.d, N, 1, N, static_cast<uint32_t>(nb)) ||
@@ -369,13 +402,24 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
       !encode_3d(&w.tmH, hidden, m.f, N, reached, kMoeTokens, static_cast<uint32_t>(nb)))
     return -2;
   const uint32_t smem_g = stream_setup<GateUpPolicy>(g.c, nb, false, false, ws, counters, status, dev);
-  const uint32_t smem_d =
-      stream_setup<DownPolicy>(w.c, nb, false, false, ws,
-                               counters + moe_reached_max(m) * ceil_div(m.f, 64), status, dev);
+  const uint32_t smem_d = stream_setup<DownPolicy>(w.c, nb, false, false, ws, nullptr, status, dev);
   if (!smem_g || !smem_d) return -3;
   w.c.late_b = 1;
   if (stream_launch<GateUpPolicy>(g, smem_g, dev, s, pdl)) return -1;
-  return stream_launch<DownPolicy>(w, smem_d, dev, s, true);
+  if (stream_launch<DownPolicy>(w, smem_d, dev, s, true)) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(m.d) / 8 * N, 128)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, moe_join_kernel, w.c, static_cast<const int*>(w.meta), residual,
+                            Y, N, m.d) == cudaSuccess
+             ? 0
+             : -1;
 }
 
 }  // namespace dyra

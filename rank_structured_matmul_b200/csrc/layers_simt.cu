@@ -208,36 +208,96 @@ int launch_act_backward_v(const T* dY, const T* Z, int act, T* dZ, T* dbias, int
 }
 
 // ----------------------------------------------------------------- router ----
-// One block per token: each warp takes every 8th expert, its lanes eight
-// consecutive products each (summed in fp32, then added in fp64: the choice
-// of experts is discrete, so logits near the border of the top k must not
-// depend on the order of a long fp32 sum). The first warp then picks the
-// largest logit top_k times.
-template <typename T>
+// Logits of four experts x four tokens per block, its 256 threads sharing d in
+// pieces of eight: eight consecutive products are summed in fp32, then added in
+// fp64 (the choice of experts is discrete: logits next to the border of the top k
+// must not depend on the order of a long fp32 sum). The last block of a token
+// group to arrive then picks, a warp per token, the largest logit top_k times.
+constexpr int kRouteTile = 4;
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* __restrict__ row, int i, int d, float (&v)[8]) {
+  if (VEC) {
+    if (sizeof(T) == 2) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + i));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row + i));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(row + i) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < d ? load_f(row[i + j]) : 0.f;
+  }
+}
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
     moe_route_kernel(MoeShape m, const T* __restrict__ X, const T* __restrict__ Wr,
-                     int* __restrict__ ids, float* __restrict__ weights) {
-  __shared__ double logit[DYRA_MOE_MAX_EXPERTS];
+                     int* __restrict__ ids, float* __restrict__ weights,
+                     double* __restrict__ logits, int* counters, int N) {
+  constexpr int R = kRouteTile;
+  __shared__ double red[8][R * R];
+  __shared__ double pick[R][DYRA_MOE_MAX_EXPERTS];
+  __shared__ int last;
   sm100::pdl_launch_dependents();  // the experts' kernel may set up meanwhile
-  const int64_t n = blockIdx.x;
+  const int e0 = blockIdx.x * R, n0 = blockIdx.y * R;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* x = X + n * m.d;
-  for (int e = warp; e < m.experts; e += 8) {
-    const T* w = Wr + static_cast<size_t>(e) * m.d;
-    double acc = 0.0;
-    for (int i = lane * 8; i < m.d; i += 256) {
-      float t = 0.f;
+  double acc[R][R] = {};
+  for (int i = threadIdx.x * 8; i < m.d; i += 256 * 8) {
+    float w[R][8], x[R][8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (i + q < m.d) t = fmaf(load_f(x[i + q]), load_f(w[i + q]), t);
-      acc += t;
+    for (int q = 0; q < R; ++q) {  // beyond the last expert or token: the last, unused
+      load8<T, VEC>(Wr + static_cast<size_t>(min(e0 + q, m.experts - 1)) * m.d, i, m.d, w[q]);
+      load8<T, VEC>(X + static_cast<size_t>(min(n0 + q, N - 1)) * m.d, i, m.d, x[q]);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) logit[e] = acc;
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+      for (int b = 0; b < R; ++b) {
+        float t = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t = fmaf(x[a][j], w[b][j], t);
+        acc[a][b] += t;
+      }
+  }
+#pragma unroll
+  for (int a = 0; a < R; ++a)
+#pragma unroll
+    for (int b = 0; b < R; ++b) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[a][b] += __shfl_xor_sync(0xffffffffu, acc[a][b], o);
+      if (lane == 0) red[warp][a * R + b] = acc[a][b];
+    }
+  __syncthreads();
+  if (threadIdx.x < R * R) {
+    double t = 0.0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += red[q][threadIdx.x];
+    const int n = n0 + threadIdx.x / R, e = e0 + threadIdx.x % R;
+    if (n < N && e < m.experts) logits[static_cast<size_t>(n) * m.experts + e] = t;
+    __threadfence();
   }
   __syncthreads();
-  if (warp != 0) return;
+  if (threadIdx.x == 0) {
+    last = atomicAdd(&counters[blockIdx.y], 1) == static_cast<int>(gridDim.x) - 1;
+    if (last) counters[blockIdx.y] = 0;
+  }
+  __syncthreads();
+  const int n = n0 + warp;
+  if (!last || warp >= R || n >= N) return;
+  __threadfence();
+  double* logit = pick[warp];
+  for (int e = lane; e < m.experts; e += 32)
+    logit[e] = __ldcg(logits + static_cast<size_t>(n) * m.experts + e);
+  __syncwarp();
   // expert 32 i + lane is this lane's i-th; a set bit of taken marks a chosen one
   unsigned taken = 0;
   double top = 0.0;
@@ -272,8 +332,8 @@ __global__ void __launch_bounds__(256)
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
   if (lane < m.top_k) {
-    ids[n * m.top_k + lane] = my_id;
-    weights[n * m.top_k + lane] = mine / sum;
+    ids[static_cast<size_t>(n) * m.top_k + lane] = my_id;
+    weights[static_cast<size_t>(n) * m.top_k + lane] = mine / sum;
   }
 }
 
@@ -403,18 +463,29 @@ template int launch_act_backward<__nv_bfloat16>(const __nv_bfloat16*, const __nv
                                                 float*, int*, int*, const DeviceInfo&,
                                                 cudaStream_t);
 
+size_t moe_logit_bytes(const MoeShape& m) {
+  return static_cast<size_t>(kRouteTokens) * m.experts * sizeof(double);
+}
+int moe_route_counters() { return kRouteTokens / kRouteTile; }
+
 template <typename T>
 int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float* weights,
-                     int64_t N, int* status, cudaStream_t s) {
-  (void)status;
-  moe_route_kernel<T><<<static_cast<unsigned>(N), 256, 0, s>>>(m, X, Wr, ids, weights);
+                     int64_t N, double* logits, int* counters, cudaStream_t s) {
+  const bool vec = m.d % 8 == 0;  // pieces of eight are whole and 16-byte aligned
+  for (int64_t n0 = 0; n0 < N; n0 += kRouteTokens) {
+    const int n = static_cast<int>(std::min<int64_t>(kRouteTokens, N - n0));
+    const dim3 grid((m.experts + kRouteTile - 1) / kRouteTile, (n + kRouteTile - 1) / kRouteTile);
+    auto kfn = vec ? moe_route_kernel<T, true> : moe_route_kernel<T, false>;
+    kfn<<<grid, 256, 0, s>>>(m, X + n0 * m.d, Wr, ids + n0 * m.top_k, weights + n0 * m.top_k,
+                             logits, counters, n);
+  }
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 template int launch_moe_route<float>(const MoeShape&, const float*, const float*, int*, float*,
-                                     int64_t, int*, cudaStream_t);
+                                     int64_t, double*, int*, cudaStream_t);
 template int launch_moe_route<__nv_bfloat16>(const MoeShape&, const __nv_bfloat16*,
-                                             const __nv_bfloat16*, int*, float*, int64_t, int*,
-                                             cudaStream_t);
+                                             const __nv_bfloat16*, int*, float*, int64_t, double*,
+                                             int*, cudaStream_t);
 
 template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,

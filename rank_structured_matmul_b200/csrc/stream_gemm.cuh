@@ -7,8 +7,9 @@
 // tiles on 148 SMs keep every SM reading to the end, where a tile per CTA would
 // leave a quarter of them idle and two tiles on one in the next wave. A tile that
 // a share's border cuts is summed from the fp32 parts its CTAs leave in a
-// workspace, in the order of the CTAs, by the one that arrives last: no CTA waits
-// for another, and the result does not depend on who is last.
+// workspace, in the order of the CTAs, by the one that arrives last (or, where a
+// tile has many parts, by a grid that follows): no CTA waits for another, and the
+// result does not depend on who is last.
 //
 // Roles as in umma_gemm.cuh: warp 0 copies (TMA, a ring of up to 12 stages),
 // warp 1 issues the MMAs into one of two accumulators, warps 2..5 take the
@@ -18,6 +19,7 @@
 // accumulator goes to the epilogue at the end of every run. A policy supplies
 //   struct Params { StreamCommon c; ... };
 //   static constexpr uint32_t kSmemBytes;   // its own shared memory, a multiple of 16
+//   static constexpr bool kWholeTiles;      // tiles are left whole where that is cheaper
 //   struct Acc;                             // an epilogue thread's state between segments
 //   static void prefetch(p);
 //   static void setup(p, sm);               // all threads, before the roles start
@@ -37,6 +39,8 @@ constexpr int kStreamThreads = 192;
 constexpr int kStreamMaxStages = 12;
 constexpr int kStreamMaxNb = 128;
 constexpr uint32_t kStreamABytes = 128u * 128u;  // 128 rows x 64 bf16
+
+constexpr int kJoinSteps = 8;
 
 struct StreamCommon {
   int nb;              // columns of a tile: a multiple of 16, at most 128
@@ -204,15 +208,20 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   Pol::shape(p, sm, tiles, nsub, ks);
   const int per_tile = nsub * ks;
   const int total = tiles * per_tile;
-  const int grid = max(1, min(static_cast<int>(gridDim.x), total / c.min_steps));
-  const int cta = static_cast<int>(blockIdx.x);
+  const int all = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+  // whole tiles where the fullest CTA then has at most kJoinSteps more steps than
+  // its share: joining the parts of a tile takes about as long as those
+  const bool cut = !Pol::kWholeTiles ||
+                   (tiles + all - 1) / all * per_tile > (total + all - 1) / all + kJoinSteps;
+  const int grid = cut ? max(1, min(all, total / c.min_steps)) : min(all, max(1, tiles));
+  const int units = cut ? total : tiles, unit = cut ? 1 : per_tile;
   StreamWalk walk;
   walk.per_tile = per_tile;
   walk.ks = ks;
   const bool works = cta < grid && total > 0;
   walk.i = walk.tile_start =
-      works ? static_cast<int>(static_cast<long long>(cta) * total / grid) : 0;
-  walk.i1 = works ? static_cast<int>(static_cast<long long>(cta + 1) * total / grid) : 0;
+      works ? static_cast<int>(static_cast<long long>(cta) * units / grid) * unit : 0;
+  walk.i1 = works ? static_cast<int>(static_cast<long long>(cta + 1) * units / grid) * unit : 0;
 
   WaitCtx w{abort_flag, c.status, c.wait_ns};
   uint32_t last_phase[kStreamMaxStages];

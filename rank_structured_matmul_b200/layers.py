@@ -101,13 +101,16 @@ def dyra_moe_destroy(p: int) -> None:
 # ---- convenience objects ----
 
 def _activation(act: str) -> int:
-    if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError("act must be one of %s, not %r" % (", ".join(ACTIVATIONS), act))
-    return ACTIVATIONS[act]
+    return code
 
 
 class _Layer:
-    """What both layers share: type, device, checks of tensors, streams."""
+    """What both layers share: type, device, checks of tensors, streams. A call of
+    a few microseconds' work is bound by what runs here, so the checks are single
+    comparisons and the current stream is read without an object for it."""
 
     def _setup(self, dtype: str) -> int:
         import torch
@@ -115,43 +118,48 @@ class _Layer:
             raise ValueError("dtype must be 'bf16' or 'f32', not %r" % (dtype,))
         self.dtype = dtype
         self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+        self.int32, self.float32 = torch.int32, torch.float32
         self.handle = None
         return DYRA_BF16 if dtype == "bf16" else DYRA_F32
 
     def _bind(self, handle: int) -> None:
         import torch
         self.handle = handle
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self.index = torch.cuda.current_device()
+        self.device = torch.device("cuda", self.index)
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def _need(self, name, t, *shape, dtype=None):
-        dtype = dtype or self.torch_dtype
-        if t is None or t.device != self.device or t.dtype != dtype or tuple(t.shape) != shape \
-                or not t.is_contiguous():
+    def _need(self, name, t, shape, dtype=None):
+        """A contiguous tensor of the shape and type on the layer's device."""
+        if t is None or t.shape != shape or t.dtype is not (dtype or self.torch_dtype) \
+                or t.get_device() != self.index or not t.is_contiguous():
             raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
-                             % (name, dtype, shape, self.device))
-
-    def _may(self, name, t, *shape):
-        if t is not None:
-            self._need(name, t, *shape)
+                             % (name, dtype or self.torch_dtype, tuple(shape), self.device))
 
     def _rows(self, X, width, name="X"):
         if X is None or X.dim() != 2:
             raise ValueError("%s must be a matrix of %d columns" % (name, width))
-        self._need(name, X, X.shape[0], width)
-        return X.shape[0]
+        N = X.shape[0]
+        self._need(name, X, (N, width))
+        return N
 
     def _on(self, stream):
-        """(context in which results are allocated, the cudaStream_t)"""
-        import torch
+        """(stream object to allocate on, or None for the current one; cudaStream_t)"""
         if stream is None:
-            return contextlib.nullcontext(), torch.cuda.current_stream(self.device).cuda_stream
+            return None, self._raw_stream(self.index)
         if isinstance(stream, int):
+            import torch
             stream = torch.cuda.ExternalStream(stream, device=self.device)
-        return torch.cuda.stream(stream), stream.cuda_stream
+        return stream, stream.cuda_stream
 
-    def _new(self, *shape, dtype=None):
-        import torch
-        return torch.empty(shape, device=self.device, dtype=dtype or self.torch_dtype)
+    def _new(self, like, on, *shapes):
+        """New tensors of the layer's type (None for a shape of None), allocated on
+        the call's stream."""
+        if on is not None:
+            import torch
+            with torch.cuda.stream(on):
+                return [like.new_empty(s) if s else None for s in shapes]
+        return [like.new_empty(s) if s else None for s in shapes]
 
     def __del__(self):
         try:
@@ -175,15 +183,17 @@ class DenseLinear(_Layer):
         residual itself."""
         code = _activation(act)
         N = self._rows(X, self.d_in)
-        self._need("W", W, self.d_out, self.d_in)
-        self._may("bias", bias, self.d_out)
-        self._may("residual", residual, N, self.d_out)
-        self._may("Y", Y, N, self.d_out)
-        ctx, s = self._on(stream)
-        with ctx:
-            if Y is None:
-                Y = self._new(N, self.d_out)
-            Z = self._new(N, self.d_out) if save_z else None
+        out = (N, self.d_out)
+        self._need("W", W, (self.d_out, self.d_in))
+        if bias is not None:
+            self._need("bias", bias, (self.d_out,))
+        if residual is not None:
+            self._need("residual", residual, out)
+        if Y is not None:
+            self._need("Y", Y, out)
+        on, s = self._on(stream)
+        new, Z = self._new(X, on, None if Y is not None else out, out if save_z else None)
+        Y = new if Y is None else Y
         dyra_dense_forward(self.handle, X, W, bias, residual, code, Y, Z, N, s)
         return (Y, Z) if save_z else Y
 
@@ -195,18 +205,17 @@ class DenseLinear(_Layer):
         code = _activation(act)
         N = self._rows(dY, self.d_out, "dY")
         if need_dW or X is not None:
-            self._need("X", X, N, self.d_in)
+            self._need("X", X, (N, self.d_in))
         if need_dX or W is not None:
-            self._need("W", W, self.d_out, self.d_in)
+            self._need("W", W, (self.d_out, self.d_in))
         if code != DYRA_ACT_NONE:
-            self._need("Z", Z, N, self.d_out)
-        ctx, s = self._on(stream)
-        with ctx:
-            dX = self._new(N, self.d_in) if need_dX else None
-            dW = self._new(self.d_out, self.d_in) if need_dW else None
-            dbias = self._new(self.d_out) if need_dbias else None
-            dZ = self._new(N, self.d_out) if code != DYRA_ACT_NONE else None
-            # freed on return; the allocator hands it out again in stream order
+            self._need("Z", Z, (N, self.d_out))
+        on, s = self._on(stream)
+        # dZ is freed on return: the allocator hands it out again in stream order
+        dX, dW, dbias, dZ = self._new(
+            dY, on, (N, self.d_in) if need_dX else None,
+            (self.d_out, self.d_in) if need_dW else None, (self.d_out,) if need_dbias else None,
+            (N, self.d_out) if code != DYRA_ACT_NONE else None)
         dyra_dense_backward(self.handle, dY, X, W, Z, code, dZ, dX, dW, dbias, N, s)
         return dX, dW, dbias
 
@@ -233,54 +242,52 @@ class MoeLayer(_Layer):
         self._bind(dyra_moe_create(d_model, d_ff, experts, top_k, _activation(act),
                                    int(bool(renorm)), code))
 
-    def _need_experts(self, Wgu, Wd):
-        self._need("Wgu", Wgu, self.experts_n, 2 * self.d_ff, self.d_model)
-        self._need("Wd", Wd, self.experts_n, self.d_model, self.d_ff)
+    def _need_experts(self, X, Wgu, Wd, residual, Y):
+        N = self._rows(X, self.d_model)
+        self._need("Wgu", Wgu, (self.experts_n, 2 * self.d_ff, self.d_model))
+        self._need("Wd", Wd, (self.experts_n, self.d_model, self.d_ff))
+        if residual is not None:
+            self._need("residual", residual, (N, self.d_model))
+        if Y is not None:
+            self._need("Y", Y, (N, self.d_model))
+        return N
+
+    def _new_routing(self, X, on, N):
+        import torch
+        with torch.cuda.stream(on) if on is not None else contextlib.nullcontext():
+            return (X.new_empty((N, self.top_k), dtype=self.int32),
+                    X.new_empty((N, self.top_k), dtype=self.float32))
 
     def route(self, X, Wr, stream=None):
         """(ids, weights): each token's top_k experts, largest logit first (the
         lower index among equals), and their softmax weights."""
-        import torch
         N = self._rows(X, self.d_model)
-        self._need("Wr", Wr, self.experts_n, self.d_model)
-        ctx, s = self._on(stream)
-        with ctx:
-            ids = self._new(N, self.top_k, dtype=torch.int32)
-            weights = self._new(N, self.top_k, dtype=torch.float32)
+        self._need("Wr", Wr, (self.experts_n, self.d_model))
+        on, s = self._on(stream)
+        ids, weights = self._new_routing(X, on, N)
         dyra_moe_route(self.handle, X, Wr, ids, weights, N, s)
         return ids, weights
 
     def experts(self, X, ids, weights, Wgu, Wd, residual=None, Y=None, stream=None):
         """sum over k of weights[n][k] * expert ids[n][k] of token n, + residual.
         Ids outside the experts (such as -1) add nothing."""
-        import torch
-        N = self._rows(X, self.d_model)
-        self._need("ids", ids, N, self.top_k, dtype=torch.int32)
-        self._need("weights", weights, N, self.top_k, dtype=torch.float32)
-        self._need_experts(Wgu, Wd)
-        self._may("residual", residual, N, self.d_model)
-        self._may("Y", Y, N, self.d_model)
-        ctx, s = self._on(stream)
-        with ctx:
-            if Y is None:
-                Y = self._new(N, self.d_model)
+        N = self._need_experts(X, Wgu, Wd, residual, Y)
+        self._need("ids", ids, (N, self.top_k), self.int32)
+        self._need("weights", weights, (N, self.top_k), self.float32)
+        on, s = self._on(stream)
+        if Y is None:
+            Y, = self._new(X, on, (N, self.d_model))
         dyra_moe_experts(self.handle, X, ids, weights, Wgu, Wd, residual, Y, N, s)
         return Y
 
     def forward(self, X, Wr, Wgu, Wd, residual=None, Y=None, stream=None):
         """The whole layer: (Y, ids, weights)."""
-        import torch
-        N = self._rows(X, self.d_model)
-        self._need("Wr", Wr, self.experts_n, self.d_model)
-        self._need_experts(Wgu, Wd)
-        self._may("residual", residual, N, self.d_model)
-        self._may("Y", Y, N, self.d_model)
-        ctx, s = self._on(stream)
-        with ctx:
-            ids = self._new(N, self.top_k, dtype=torch.int32)
-            weights = self._new(N, self.top_k, dtype=torch.float32)
-            if Y is None:
-                Y = self._new(N, self.d_model)
+        N = self._need_experts(X, Wgu, Wd, residual, Y)
+        self._need("Wr", Wr, (self.experts_n, self.d_model))
+        on, s = self._on(stream)
+        ids, weights = self._new_routing(X, on, N)
+        if Y is None:
+            Y, = self._new(X, on, (N, self.d_model))
         dyra_moe_forward(self.handle, X, Wr, Wgu, Wd, residual, Y, ids, weights, N, s)
         return Y, ids, weights
 

@@ -88,7 +88,7 @@ def _fake(cls, **attrs):
     before any call of the library."""
     x = cls.__new__(cls)
     x._setup("bf16")
-    x.device = torch.device("cpu")
+    x.device, x.index = torch.device("cpu"), -1
     for k, v in attrs.items():
         setattr(x, k, v)
     return x
