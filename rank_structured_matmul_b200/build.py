@@ -29,7 +29,7 @@ LIB_PATH = os.path.join(HERE, "libdyra.so")
 DEBUG_LIB_PATH = os.path.join(HERE, "libdyra_debug.so")
 
 SOURCES = ["dyra_api.cu", "kernels_umma.cu", "kernels_simt.cu", "layers_api.cu", "layers_simt.cu",
-           "layers_umma.cu", "layers_moe_umma.cu"]
+           "layers_f32.cu", "layers_umma.cu", "layers_moe_umma.cu"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH_FLAGS + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                            "-Xptxas", "-warn-spills", "-I", INCLUDE, "-I", CSRC]

@@ -30,8 +30,9 @@ struct LinearGemm {
   int* status = nullptr;
 };
 
-// CUDA-core product (layers_simt.cu): T = float or __nv_bfloat16.
-template <typename T>
+// CUDA-core products: fp32 (layers_f32.cu), and bf16 for DYRA_KERNELS=simt
+// (layers_simt.cu).
+int launch_linear_f32(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 
 // Tensor-core product of bf16 operands (layers_umma.cu). pdl: a programmatic
@@ -70,7 +71,7 @@ int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float
 template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
                             const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
-                            float* part, int* status, cudaStream_t s);
+                            float* part, int* status, cudaStream_t s, bool pdl);
 
 // Tensor-core experts for N <= kMoeTokens tokens (layers_moe_umma.cu). hidden:
 // moe_reached_max x kMoeTokens x f values; ws and counters (zero between calls)

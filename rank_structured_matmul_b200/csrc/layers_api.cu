@@ -95,8 +95,8 @@ int launched(int rc) {
 }
 
 int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s, bool pdl) {
-  if (p->dtype == DYRA_F32) return launch_linear_simt<float>(g, p->dev, s);
-  if (p->simt) return launch_linear_simt<__nv_bfloat16>(g, p->dev, s);
+  if (p->dtype == DYRA_F32) return launch_linear_f32(g, p->dev, s);
+  if (p->simt) return launch_linear_simt(g, p->dev, s);
   return launch_linear_umma(g, p->dev, s, pdl);
 }
 
@@ -145,7 +145,7 @@ int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
   return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
-                                    static_cast<T*>(p->hidden), p->part, p->status, s);
+                                    static_cast<T*>(p->hidden), p->part, p->status, s, pdl);
 }
 
 // The shared checks of the calls on N tokens: DYRA_OK to go on.

@@ -1,0 +1,357 @@
+// layers_f32.cu - the dense layer's fp32 products on the CUDA cores: plain FFMA
+// (TF32 tensor cores would lose ~1e-3).
+//
+// An Out tile of BT x BT on 256 threads of (BT/16)^2 values each, k in steps of 32
+// through a ring of three shared-memory buffers filled by asynchronous copies.
+// An operand's tile is kept as it is stored, rows of k (K-major) or rows of k over
+// consecutive m (MN-major), so the copies are 16 bytes where the stored rows are
+// 16-byte aligned and single values otherwise (odd sizes). Small products are
+// bound by the latency of their few steps: a tile's steps are then shared by a
+// cluster of cs CTAs, whose parts meet in distributed shared memory, in order.
+#include <algorithm>
+
+#include "layers.h"
+#include "layers_math.cuh"
+#include "sm100.cuh"
+
+namespace dyra {
+
+namespace {
+
+using sm100::cluster_ctarank;
+using sm100::cluster_sync_all;
+using sm100::mapa_shared;
+using sm100::smem_u32;
+
+constexpr int kBk = 32, kRing = 3;
+
+template <int BT>
+struct F32Tile {
+  static constexpr int V = BT / 16;                 // values per thread and side
+  static constexpr int LdK = kBk + 4;               // K-major: [BT][LdK]
+  static constexpr int LdM = BT + 4;                // MN-major: [kBk][LdM]
+  static constexpr int Buf = BT * LdK > kBk * LdM ? BT * LdK : kBk * LdM;  // floats
+  static constexpr int Part = BT * BT;
+  static constexpr int Floats = 2 * kRing * Buf > Part ? 2 * kRing * Buf : Part;
+};
+
+// 4 bytes, or zero
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(in ? 4 : 0)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The BT x kBk tile at (r0, k0) of an operand of `rows` rows and K columns.
+template <int BT, bool MN, bool VEC>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const float* __restrict__ src, int64_t rows,
+                                          int64_t K, int64_t r0, int64_t k0) {
+  using S = F32Tile<BT>;
+  constexpr int W = VEC ? 4 : 1;  // values per copy
+  constexpr int Count = BT * kBk / W;
+#pragma unroll
+  for (int i = 0; i < (Count + 255) / 256; ++i) {
+    const int idx = threadIdx.x + 256 * i;
+    if (Count % 256 && idx >= Count) break;
+    int r, k;
+    if (MN) {
+      r = idx % (BT / W) * W;
+      k = idx / (BT / W);
+    } else {
+      k = idx % (kBk / W) * W;
+      r = idx / (kBk / W);
+    }
+    const int64_t gr = r0 + r, gk = k0 + k;
+    const bool in = gr < rows && gk < K;
+    const float* from = src + (in ? (MN ? gk * rows + gr : gr * K + gk) : 0);
+    const uint32_t to = dst + 4u * static_cast<uint32_t>(MN ? k * S::LdM + r : r * S::LdK + k);
+    if (VEC)
+      sm100::cp_async_16(to, from, in ? 16u : 0u);
+    else
+      cp_async_4(to, from, in);
+  }
+}
+
+// A thread's V rows of a side: t + 16 v of a K-major operand, 4 t + 64 (v / 4) + v % 4
+// (V >= 4) or V t + v of an MN-major one.
+template <int BT, bool MN>
+__device__ __forceinline__ int side_row(int t, int v) {
+  constexpr int V = F32Tile<BT>::V;
+  if (!MN) return t + 16 * v;
+  return V >= 4 ? 4 * t + 64 * (v / 4) + v % 4 : V * t + v;
+}
+// Two fp32 FMAs in one instruction on the halves of 64-bit registers, which halves
+// the issue slots of the inner product (dW of 512 rows, 2048 -> 2048: 150 -> 109 us
+// with 128 tiles; the forward, bound by its shared-memory loads, is as before).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ f32x2 twice(float v) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+
+// A's side of the product, four k of a buffer: acc(y, x) += sum over k of a b.
+// K-major A (then B is K-major too): the halves are even and odd k, both operands
+// as they lie; MN-major A: the halves are two neighbouring x, b goes to both.
+template <int BT, bool AMN, bool BMN>
+struct Product {
+  using S = F32Tile<BT>;
+  static constexpr int V = S::V, XN = AMN ? V / 2 : V;
+  static_assert(AMN || !BMN, "a K-major A comes with a K-major B");
+  f32x2 acc[V][XN];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int y = 0; y < V; ++y)
+#pragma unroll
+      for (int x = 0; x < XN; ++x) acc[y][x] = 0ull;
+  }
+  __device__ __forceinline__ void step(const float* as, const float* bs, int tx, int ty, int k) {
+    if constexpr (!AMN) {
+      ulonglong2 a[V], b[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        a[v] = *reinterpret_cast<const ulonglong2*>(as + (tx + 16 * v) * S::LdK + k);
+        b[v] = *reinterpret_cast<const ulonglong2*>(bs + (ty + 16 * v) * S::LdK + k);
+      }
+#pragma unroll
+      for (int y = 0; y < V; ++y)
+#pragma unroll
+        for (int x = 0; x < V; ++x) fma2(acc[y][x], a[x].x, b[y].x);
+#pragma unroll
+      for (int y = 0; y < V; ++y)
+#pragma unroll
+        for (int x = 0; x < V; ++x) fma2(acc[y][x], a[x].y, b[y].y);
+    } else {
+      float b[4][V];
+      if constexpr (!BMN) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float4 q = *reinterpret_cast<const float4*>(bs + (ty + 16 * v) * S::LdK + k);
+          b[0][v] = q.x, b[1][v] = q.y, b[2][v] = q.z, b[3][v] = q.w;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x2 a[XN];
+        const float* row = as + (k + q) * S::LdM;
+        if constexpr (V >= 4) {
+#pragma unroll
+          for (int g = 0; g < V / 4; ++g) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(row + 4 * tx + 64 * g);
+            a[2 * g] = w.x, a[2 * g + 1] = w.y;
+          }
+        } else {
+          a[0] = *reinterpret_cast<const f32x2*>(row + 2 * tx);
+        }
+        if constexpr (BMN) {
+          const float* br = bs + (k + q) * S::LdM;
+          if constexpr (V >= 4) {
+#pragma unroll
+            for (int g = 0; g < V / 4; ++g) {
+              const float4 w = *reinterpret_cast<const float4*>(br + 4 * ty + 64 * g);
+              b[q][4 * g] = w.x, b[q][4 * g + 1] = w.y, b[q][4 * g + 2] = w.z;
+              b[q][4 * g + 3] = w.w;
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) b[q][v] = br[V * ty + v];
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < V; ++y) {
+          const f32x2 by = twice(b[q][y]);
+#pragma unroll
+          for (int x = 0; x < XN; ++x) fma2(acc[y][x], a[x], by);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float value(int y, int x) const {
+    if constexpr (AMN) {
+      const float2 h = halves(acc[y][x / 2]);
+      return x & 1 ? h.y : h.x;
+    } else {
+      const float2 h = halves(acc[y][x]);
+      return h.x + h.y;
+    }
+  }
+};
+
+__device__ __forceinline__ void finish_f32(const LinearGemm& g, int64_t j, int64_t m, float z) {
+  const size_t at = static_cast<size_t>(j) * g.M + m;
+  if (!sm100::in_bounds(g.status, at, 1, static_cast<size_t>(g.J) * g.M)) return;
+  if (g.bias) z += static_cast<const float*>(g.bias)[m];
+  if (g.Z) static_cast<float*>(g.Z)[at] = z;
+  float y = z;
+  with_act(g.act, [&](auto tag) { y = act_f<decltype(tag)::value>(z); });
+  if (g.residual) y += static_cast<const float*>(g.residual)[at];
+  static_cast<float*>(g.Out)[at] = y;
+}
+
+template <int BT, bool AMN, bool BMN, bool VEC>
+__global__ void __launch_bounds__(256)
+    linear_f32_kernel(const __grid_constant__ LinearGemm g, int64_t m_tiles, int cs) {
+  using S = F32Tile<BT>;
+  constexpr int V = S::V;
+  extern __shared__ __align__(16) float smem[];
+  const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t tile = blockIdx.x / cs;
+  const int64_t jt = tile / m_tiles;
+  const int64_t m0 = (tile - jt * m_tiles) * BT, j0 = jt * BT;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float* A = static_cast<const float*>(g.A);
+  const float* B = static_cast<const float*>(g.B);
+  const int64_t steps = (g.K + kBk - 1) / kBk;
+  const int64_t s0 = rank * steps / cs, s1 = (rank + 1) * steps / cs;
+  const uint32_t base = smem_u32(smem);
+  auto issue = [&](int64_t s) {
+    if (s < s1) {
+      const uint32_t at = base + static_cast<uint32_t>((s - s0) % kRing) * (2u * S::Buf * 4u);
+      copy_tile<BT, AMN, VEC>(at, A, g.M, g.K, m0, s * kBk);
+      copy_tile<BT, BMN, VEC>(at + S::Buf * 4u, B, g.J, g.K, j0, s * kBk);
+    }
+    sm100::cp_async_commit();  // one group per step, empty beyond the last
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) issue(s0 + i);
+  Product<BT, AMN, BMN> sum;
+  sum.clear();
+  for (int64_t s = s0; s < s1; ++s) {
+    cp_async_wait<kRing - 2>();
+    __syncthreads();  // step s has landed, and step s - 1's buffer is no longer read
+    issue(s + kRing - 1);
+    const float* as = smem + static_cast<size_t>((s - s0) % kRing) * 2 * S::Buf;
+    const float* bs = as + S::Buf;
+#pragma unroll
+    for (int k = 0; k < kBk; k += 4) sum.step(as, bs, tx, ty, k);
+  }
+  if (cs == 1) {
+#pragma unroll
+    for (int y = 0; y < V; ++y) {
+      const int64_t j = j0 + side_row<BT, BMN>(ty, y);
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        const int64_t m = m0 + side_row<BT, AMN>(tx, x);
+        if (j < g.J && m < g.M) finish_f32(g, j, m, sum.value(y, x));
+      }
+    }
+    return;
+  }
+  cp_async_wait<0>();
+  __syncthreads();  // the buffers hold the part [BT][BT] now
+#pragma unroll
+  for (int y = 0; y < V; ++y)
+#pragma unroll
+    for (int x = 0; x < V; ++x)
+      smem[side_row<BT, BMN>(ty, y) * BT + side_row<BT, AMN>(tx, x)] = sum.value(y, x);
+  cluster_sync_all();
+  const int r0 = rank * BT / cs, r1 = (rank + 1) * BT / cs;
+  for (int i = r0 * BT + static_cast<int>(threadIdx.x); i < r1 * BT; i += 256) {
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = q < cs ? ld_shared_cluster(mapa_shared(base + 4u * i, static_cast<uint32_t>(q))) : 0.f;
+    float z = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < cs) z += v[q];
+    const int64_t j = j0 + i / BT, m = m0 + i % BT;
+    if (j < g.J && m < g.M) finish_f32(g, j, m, z);
+  }
+  cluster_sync_all();  // no CTA leaves while its part is read
+}
+
+template <int BT, bool AMN, bool BMN, bool VEC>
+int launch_tile(const LinearGemm& g, int cs, const DeviceInfo& dev, cudaStream_t s) {
+  auto kfn = linear_f32_kernel<BT, AMN, BMN, VEC>;
+  static KernelSetup setup;
+  const int d = dev.device;
+  if (d < 0 || d >= kMaxDevices) return -1;
+  constexpr uint32_t smem = F32Tile<BT>::Floats * 4;
+  if (smem > setup.smem[d].load()) {
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return -1;
+    setup.smem[d].store(smem);
+  }
+  const int64_t mt = (g.M + BT - 1) / BT, jt = (g.J + BT - 1) / BT;
+  if (mt * jt * cs > 0x7fffffffll) return -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(mt * jt * cs));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kfn, g, mt, cs) == cudaSuccess ? 0 : -1;
+}
+
+template <int BT>
+int launch_bt(const LinearGemm& g, int cs, const DeviceInfo& dev, cudaStream_t s) {
+  // 16-byte copies need every stored row to start on 16 bytes
+  const int64_t la = g.a_mn ? g.M : g.K, lb = g.b_mn ? g.J : g.K;
+  const bool vec = la % 4 == 0 && lb % 4 == 0;
+  if (g.a_mn && g.b_mn)
+    return vec ? launch_tile<BT, true, true, true>(g, cs, dev, s)
+               : launch_tile<BT, true, true, false>(g, cs, dev, s);
+  if (g.a_mn)
+    return vec ? launch_tile<BT, true, false, true>(g, cs, dev, s)
+               : launch_tile<BT, true, false, false>(g, cs, dev, s);
+  return vec ? launch_tile<BT, false, false, true>(g, cs, dev, s)
+             : launch_tile<BT, false, false, false>(g, cs, dev, s);
+}
+
+}  // namespace
+
+// Tile and cluster by a model in microseconds, fitted to 64 x 256 -> 256 up to
+// 1024 x 1024 -> 1024 and 512 x 2048 -> 2048: a step of a 128, 64 or 32 tile takes
+// its SM about 3.9, 1.25 or 0.5, and joining a cluster's parts 6, 1.5 or 0.7 (512 x
+// 512 -> 512: 14.8 with 64 tiles in clusters of 4, 25.6 alone, 24.3 with 128 tiles).
+int launch_linear_f32(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s) {
+  const int64_t steps = (g.K + kBk - 1) / kBk;
+  int best_bt = 128, best_cs = 1;
+  double best = -1.0;
+  for (int bt : {128, 64, 32}) {
+    const int64_t tiles = ((g.M + bt - 1) / bt) * ((g.J + bt - 1) / bt);
+    const double step = bt == 128 ? 3.9 : bt == 64 ? 1.25 : 0.5;
+    const double join = bt == 128 ? 6.0 : bt == 64 ? 1.5 : 0.7;
+    for (int cs = 1; cs <= 8 && cs <= steps; cs *= 2) {
+      if (cs > 1 && tiles * cs > 2 * dev.sm_count) break;
+      const double rounds = static_cast<double>((tiles * cs + dev.sm_count - 1) / dev.sm_count);
+      const double us = rounds * step * static_cast<double>((steps + cs - 1) / cs) +
+                        (cs > 1 ? join : 0.0);
+      if (best < 0.0 || us < best) {
+        best = us;
+        best_bt = bt;
+        best_cs = cs;
+      }
+    }
+  }
+  if (best_bt == 128) return launch_bt<128>(g, best_cs, dev, s);
+  if (best_bt == 64) return launch_bt<64>(g, best_cs, dev, s);
+  return launch_bt<32>(g, best_cs, dev, s);
+}
+
+}  // namespace dyra

@@ -1,6 +1,6 @@
-// layers_simt.cu - CUDA-core kernels of the dense and expert layers: the fp32
-// products (fp32 accuracy needs plain FFMA; TF32 would lose ~1e-3), the
-// activation's backward with its column sums, and the router.
+// layers_simt.cu - CUDA-core kernels of the dense and expert layers: the
+// activation's backward with its column sums, the router, the experts of fp32
+// handles, and the debugging variant of the bf16 products.
 #include <algorithm>
 
 #include "layers.h"
@@ -11,112 +11,60 @@ namespace dyra {
 
 namespace {
 
-// ------------------------------------------------------------ dense gemm ----
-// Out[j][m] tile of 64 G x 64 G, 256 threads with 4 G x 4 G values each, k in
-// steps of 16 through two shared-memory buffers: the loads of step s + 1 are in
-// flight while step s is multiplied. Loads are element-wise (rows of odd
-// length have no common alignment) with consecutive threads on the stored
-// matrix's contiguous index.
-constexpr int kSimtBk = 16;
+// ------------------------------------------------------- bf16 dense gemm ----
+// The debugging variant of the bf16 products: 64 x 64 of Out per block of 256
+// threads, k in steps of 16 through shared memory in fp32.
+constexpr int kSimtBt = 64, kSimtBk = 16;
 
-template <typename T, bool AMN, bool BMN, int G>
-__global__ void __launch_bounds__(256)
-    linear_simt_kernel(LinearGemm g, int64_t m_tiles) {
-  constexpr int BT = 64 * G;
-  constexpr int PER = BT * kSimtBk / 256;
-  __shared__ __align__(16) float As[2][kSimtBk][BT + 4];
-  __shared__ __align__(16) float Bs[2][kSimtBk][BT + 4];
+template <bool AMN, bool BMN>
+__global__ void __launch_bounds__(256) linear_simt_kernel(LinearGemm g, int64_t m_tiles) {
+  using T = __nv_bfloat16;
+  __shared__ float As[kSimtBk][kSimtBt + 1];
+  __shared__ float Bs[kSimtBk][kSimtBt + 1];
   const T* __restrict__ A = static_cast<const T*>(g.A);
   const T* __restrict__ B = static_cast<const T*>(g.B);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t jt = blockIdx.x / m_tiles;
-  const int64_t m0 = (blockIdx.x - jt * m_tiles) * BT, j0 = jt * BT;
-  float ra[PER], rb[PER];
-  auto fetch = [&](int64_t k0) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int idx = threadIdx.x + 256 * i;
-      const int ka = AMN ? idx / BT : idx % kSimtBk, ma = AMN ? idx % BT : idx / kSimtBk;
-      const int kb = BMN ? idx / BT : idx % kSimtBk, jb = BMN ? idx % BT : idx / kSimtBk;
+  const int64_t m0 = (blockIdx.x - jt * m_tiles) * kSimtBt, j0 = jt * kSimtBt;
+  float acc[4][4] = {};
+  for (int64_t k0 = 0; k0 < g.K; k0 += kSimtBk) {
+    for (int idx = threadIdx.x; idx < kSimtBt * kSimtBk; idx += 256) {
+      const int ka = AMN ? idx / kSimtBt : idx % kSimtBk, ma = AMN ? idx % kSimtBt : idx / kSimtBk;
+      const int kb = BMN ? idx / kSimtBt : idx % kSimtBk, jb = BMN ? idx % kSimtBt : idx / kSimtBk;
       const int64_t gm = m0 + ma, gka = k0 + ka, gj = j0 + jb, gkb = k0 + kb;
-      ra[i] = gm < g.M && gka < g.K ? load_f(A[AMN ? gka * g.M + gm : gm * g.K + gka]) : 0.f;
-      rb[i] = gj < g.J && gkb < g.K ? load_f(B[BMN ? gkb * g.J + gj : gj * g.K + gkb]) : 0.f;
+      As[ka][ma] = gm < g.M && gka < g.K ? load_f(A[AMN ? gka * g.M + gm : gm * g.K + gka]) : 0.f;
+      Bs[kb][jb] = gj < g.J && gkb < g.K ? load_f(B[BMN ? gkb * g.J + gj : gj * g.K + gkb]) : 0.f;
     }
-  };
-  auto stash = [&](int buf) {
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int idx = threadIdx.x + 256 * i;
-      As[buf][AMN ? idx / BT : idx % kSimtBk][AMN ? idx % BT : idx / kSimtBk] = ra[i];
-      Bs[buf][BMN ? idx / BT : idx % kSimtBk][BMN ? idx % BT : idx / kSimtBk] = rb[i];
-    }
-  };
-  float acc[4 * G][4 * G] = {};
-  fetch(0);
-  stash(0);
-  __syncthreads();
-  int buf = 0;
-  for (int64_t k0 = 0; k0 < g.K; k0 += kSimtBk, buf ^= 1) {
-    const bool more = k0 + kSimtBk < g.K;
-    if (more) fetch(k0 + kSimtBk);
+    for (int k = 0; k < kSimtBk; ++k)
 #pragma unroll
-    for (int k = 0; k < kSimtBk; ++k) {
-      float a[4 * G], b[4 * G];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int q = 0; q < G; ++q) {
-        const float4 av = *reinterpret_cast<const float4*>(&As[buf][k][64 * q + 4 * tx]);
-        const float4 bv = *reinterpret_cast<const float4*>(&Bs[buf][k][64 * q + 4 * ty]);
-        a[4 * q] = av.x, a[4 * q + 1] = av.y, a[4 * q + 2] = av.z, a[4 * q + 3] = av.w;
-        b[4 * q] = bv.x, b[4 * q + 1] = bv.y, b[4 * q + 2] = bv.z, b[4 * q + 3] = bv.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 4 * G; ++j)
-#pragma unroll
-        for (int m = 0; m < 4 * G; ++m) acc[j][m] = fmaf(b[j], a[m], acc[j][m]);
-    }
-    if (more) stash(buf ^ 1);
+        for (int m = 0; m < 4; ++m)
+          acc[j][m] = fmaf(Bs[k][ty + 16 * j], As[k][tx + 16 * m], acc[j][m]);
     __syncthreads();
   }
   const T* __restrict__ bias = static_cast<const T*>(g.bias);
   const T* residual = static_cast<const T*>(g.residual);  // may be Out: no __restrict__
-  T* Out = static_cast<T*>(g.Out);
-  T* Z = static_cast<T*>(g.Z);
-  with_act(g.act, [&](auto tag) {
-    constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-    for (int j = 0; j < 4 * G; ++j) {
-      const int64_t gj = j0 + 64 * (j / 4) + 4 * ty + (j & 3);
-      if (gj >= g.J) continue;
+  for (int j = 0; j < 4; ++j) {
+    const int64_t gj = j0 + ty + 16 * j;
+    if (gj >= g.J) continue;
 #pragma unroll
-      for (int m = 0; m < 4 * G; ++m) {
-        const int64_t gm = m0 + 64 * (m / 4) + 4 * tx + (m & 3);
-        if (gm >= g.M) continue;
-        const size_t at = static_cast<size_t>(gj) * g.M + gm;
-        if (!sm100::in_bounds(g.status, at, 1, static_cast<size_t>(g.J) * g.M)) continue;
-        float z = acc[j][m];
-        if (bias) z += load_f(bias[gm]);
-        if (Z) Z[at] = store_f<T>(z);
-        float y = act_f<ACT, kFastMath<T>>(z);
-        if (residual) y += load_f(residual[at]);
-        Out[at] = store_f<T>(y);
-      }
+    for (int m = 0; m < 4; ++m) {
+      const int64_t gm = m0 + tx + 16 * m;
+      if (gm >= g.M) continue;
+      const size_t at = static_cast<size_t>(gj) * g.M + gm;
+      if (!sm100::in_bounds(g.status, at, 1, static_cast<size_t>(g.J) * g.M)) continue;
+      float z = acc[j][m];
+      if (bias) z += load_f(bias[gm]);
+      if (g.Z) static_cast<T*>(g.Z)[at] = store_f<T>(z);
+      with_act(g.act, [&](auto tag) { z = act_f<decltype(tag)::value, true>(z); });
+      if (residual) z += load_f(residual[at]);
+      static_cast<T*>(g.Out)[at] = store_f<T>(z);
     }
-  });
-}
-
-template <typename T, int G>
-int launch_linear_simt_g(const LinearGemm& g, cudaStream_t s) {
-  constexpr int BT = 64 * G;
-  const int64_t mt = (g.M + BT - 1) / BT, jt = (g.J + BT - 1) / BT;
-  if (mt * jt > 0x7fffffffll) return -1;
-  const dim3 grid(static_cast<unsigned>(mt * jt));
-  if (g.a_mn && g.b_mn)
-    linear_simt_kernel<T, true, true, G><<<grid, 256, 0, s>>>(g, mt);
-  else if (g.a_mn)
-    linear_simt_kernel<T, true, false, G><<<grid, 256, 0, s>>>(g, mt);
-  else
-    linear_simt_kernel<T, false, false, G><<<grid, 256, 0, s>>>(g, mt);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  }
 }
 
 // ---------------------------------------------------- activation backward ----
@@ -136,27 +84,37 @@ __global__ void __launch_bounds__(256)
   const int col = (blockIdx.x * 32 + lane) * V;
   float sum[V] = {};
   if (col < d_out) {
-    for (int64_t r = static_cast<int64_t>(blockIdx.y) * 8 + rl; r < N;
-         r += static_cast<int64_t>(gridDim.y) * 8) {
-      const size_t at = static_cast<size_t>(r) * d_out + col;
-      if (!sm100::in_bounds(status, at, V, static_cast<size_t>(N) * d_out)) continue;
-      const P g = *reinterpret_cast<const P*>(dY + at);
-      P out;
-      if (ACT != DYRA_ACT_NONE) {
-        const P z = *reinterpret_cast<const P*>(Z + at);
+    constexpr int kRows = 4;  // rows of a thread in flight
+    const int64_t stride = static_cast<int64_t>(gridDim.y) * 8;
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * 8 + rl; r0 < N; r0 += kRows * stride) {
+      P g[kRows], z[kRows];
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t r = r0 + u * stride;
+        const size_t at = static_cast<size_t>(r) * d_out + col;
+        if (r < N && sm100::in_bounds(status, at, V, static_cast<size_t>(N) * d_out)) {
+          g[u] = *reinterpret_cast<const P*>(dY + at);
+          if (ACT != DYRA_ACT_NONE) z[u] = *reinterpret_cast<const P*>(Z + at);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        const int64_t r = r0 + u * stride;
+        const size_t at = static_cast<size_t>(r) * d_out + col;
+        if (r >= N || !sm100::in_bounds(status, at, V, static_cast<size_t>(N) * d_out)) continue;
+        P out;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+          float d = load_f(g[u].v[i]);
           // a zero slope of the ReLU is a zero gradient, whatever dY holds
-          const float d = ACT == DYRA_ACT_RELU
-                              ? (load_f(z.v[i]) > 0.f ? load_f(g.v[i]) : 0.f)
-                              : load_f(g.v[i]) * act_grad_f<ACT, kFastMath<T>>(load_f(z.v[i]));
+          if (ACT == DYRA_ACT_RELU)
+            d = load_f(z[u].v[i]) > 0.f ? d : 0.f;
+          else if (ACT != DYRA_ACT_NONE)
+            d *= act_grad_f<ACT, kFastMath<T>>(load_f(z[u].v[i]));
           sum[i] += d;
           out.v[i] = store_f<T>(d);
         }
-        *reinterpret_cast<P*>(dZ + at) = out;
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += load_f(g.v[i]);
+        if (ACT != DYRA_ACT_NONE) *reinterpret_cast<P*>(dZ + at) = out;
       }
     }
   }
@@ -268,14 +226,24 @@ __global__ void __launch_bounds__(256)
         acc[a][b] += t;
       }
   }
+  // the sixteen sums over the warp: at each step a lane keeps half of its values
+  // and hands the other half to its partner, so lane l ends with value l / 2
+  double v[R * R];
 #pragma unroll
   for (int a = 0; a < R; ++a)
 #pragma unroll
-    for (int b = 0; b < R; ++b) {
+    for (int b = 0; b < R; ++b) v[a * R + b] = acc[a][b];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc[a][b] += __shfl_xor_sync(0xffffffffu, acc[a][b], o);
-      if (lane == 0) red[warp][a * R + b] = acc[a][b];
+  for (int o = 16, n = R * R / 2; n > 0; o >>= 1, n >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const double give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  if ((lane & 1) == 0) red[warp][lane >> 1] = v[0];
   __syncthreads();
   if (threadIdx.x < R * R) {
     double t = 0.0;
@@ -339,16 +307,67 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- experts ----
 // CUDA-core experts: a warp per output row of one expert, over the slots
-// (token, k) that name it, eight at a time: each weight is read once per eight
-// slots. STAGE 0: hidden[slot] = act(g) u over rows f; STAGE 1: part[slot] over
-// rows d. The slots of the block's expert are listed in order first.
-template <typename T, int STAGE>
+// (token, k) that name it, up to eight at a time: each weight is read once per
+// eight slots. STAGE 0: hidden[slot] = act(g) u over rows f; STAGE 1: part[slot]
+// over rows d. The slots of the block's expert are listed in order first. VEC: the
+// rows are whole 16-byte pieces.
+template <typename T, int STAGE, bool VEC, int NS>
+__device__ __forceinline__ void expert_row(const MoeShape& m, const T* __restrict__ In,
+                                           const T* __restrict__ w0, const T* __restrict__ w1,
+                                           const int* list, int K, int rows, int row, int lane,
+                                           T* __restrict__ hidden, float* __restrict__ part,
+                                           size_t extent, int* status) {
+  constexpr int W = VEC ? 16 / sizeof(T) : 1;
+  struct alignas(W * sizeof(T)) P {
+    T v[W];
+  };
+  const T* x[NS];
+  float a0[NS] = {}, a1[NS] = {};
+#pragma unroll
+  for (int q = 0; q < NS; ++q)
+    x[q] = In + static_cast<size_t>(STAGE == 0 ? list[q] / m.top_k : list[q]) * K;
+#pragma unroll 4
+  for (int i = lane * W; i < K; i += 32 * W) {
+    const P p0 = *reinterpret_cast<const P*>(w0 + i);
+    P p1 = p0;
+    if (STAGE == 0) p1 = *reinterpret_cast<const P*>(w1 + i);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+      const P px = *reinterpret_cast<const P*>(x[q] + i);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        a0[q] = fmaf(load_f(p0.v[j]), load_f(px.v[j]), a0[q]);
+        if (STAGE == 0) a1[q] = fmaf(load_f(p1.v[j]), load_f(px.v[j]), a1[q]);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NS; ++q) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a0[q] += __shfl_xor_sync(0xffffffffu, a0[q], o);
+      if (STAGE == 0) a1[q] += __shfl_xor_sync(0xffffffffu, a1[q], o);
+    }
+    const size_t at = static_cast<size_t>(list[q]) * rows + row;
+    if (lane != 0 || !sm100::in_bounds(status, at, 1, extent)) continue;
+    if (STAGE == 0)
+      with_act(m.act, [&](auto tag) {
+        hidden[at] = store_f<T>(act_f<decltype(tag)::value, kFastMath<T>>(a0[q]) * a1[q]);
+      });
+    else
+      part[at] = a0[q];
+  }
+}
+
+template <typename T, int STAGE, bool VEC>
 __global__ void __launch_bounds__(256)
     moe_expert_kernel(MoeShape m, const T* __restrict__ In, const int* __restrict__ ids,
                       const T* __restrict__ W, T* __restrict__ hidden, float* __restrict__ part,
-                      int N, int act, int* status) {
+                      int N, int* status) {
   __shared__ int list[kMoeTokens * DYRA_MOE_MAX_TOP_K];
   __shared__ int count;
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int e = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slots = N * m.top_k;
@@ -365,50 +384,24 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int nsl = count;
-  if (nsl == 0) return;
   const int rows = STAGE == 0 ? m.f : m.d, K = STAGE == 0 ? m.d : m.f;
   const size_t wrows = STAGE == 0 ? 2 * static_cast<size_t>(m.f) : m.d;
   const T* We = W + wrows * e * K;
+  const size_t extent = static_cast<size_t>(slots) * rows;
   const int row = blockIdx.x * 8 + warp;
   if (row >= rows) return;
   const T* w0 = We + static_cast<size_t>(row) * K;
   const T* w1 = STAGE == 0 ? We + static_cast<size_t>(m.f + row) * K : w0;
-  for (int s0 = 0; s0 < nsl; s0 += 8) {
-    float a0[8] = {}, a1[8] = {};
-    const T* x[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int slot = list[min(s0 + q, nsl - 1)];
-      x[q] = In + static_cast<size_t>(STAGE == 0 ? slot / m.top_k : slot) * K;
-    }
-    for (int i = lane; i < K; i += 32) {
-      const float v0 = load_f(w0[i]), v1 = STAGE == 0 ? load_f(w1[i]) : 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float xv = load_f(x[q][i]);
-        a0[q] = fmaf(v0, xv, a0[q]);
-        if (STAGE == 0) a1[q] = fmaf(v1, xv, a1[q]);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        a0[q] += __shfl_xor_sync(0xffffffffu, a0[q], o);
-        if (STAGE == 0) a1[q] += __shfl_xor_sync(0xffffffffu, a1[q], o);
-      }
-      if (lane == 0 && s0 + q < nsl) {
-        const size_t at = static_cast<size_t>(list[s0 + q]) * rows + row;
-        if (!sm100::in_bounds(status, at, 1, static_cast<size_t>(slots) * rows)) continue;
-        if (STAGE == 0)
-          with_act(act, [&](auto tag) {
-            hidden[at] = store_f<T>(act_f<decltype(tag)::value, kFastMath<T>>(a0[q]) * a1[q]);
-          });
-        else
-          part[at] = a0[q];
-      }
-    }
-  }
+  int s0 = 0;
+  for (; s0 + 8 <= nsl; s0 += 8)
+    expert_row<T, STAGE, VEC, 8>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
+                                 status);
+  for (; s0 + 3 <= nsl; s0 += 3)
+    expert_row<T, STAGE, VEC, 3>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
+                                 status);
+  for (; s0 < nsl; ++s0)
+    expert_row<T, STAGE, VEC, 1>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
+                                 status);
 }
 
 // Y[n] = sum over k, in order, of weights[n][k] part[n][k] + residual[n]
@@ -417,6 +410,8 @@ __global__ void __launch_bounds__(256)
     moe_combine_kernel(MoeShape m, const int* __restrict__ ids, const float* __restrict__ weights,
                        const float* __restrict__ part, const T* residual, T* Y, int N,
                        int* status) {
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int n = blockIdx.y, i = blockIdx.x * 256 + threadIdx.x;
   if (i >= m.d) return;
   float acc = 0.f;
@@ -433,15 +428,18 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-// 128 x 128 tiles once they fill the SMs; below that 64 x 64 tiles spread the
-// work over more of them.
-template <typename T>
-int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s) {
-  const int64_t big = ((g.M + 127) / 128) * ((g.J + 127) / 128);
-  return big >= dev.sm_count ? launch_linear_simt_g<T, 2>(g, s) : launch_linear_simt_g<T, 1>(g, s);
+int launch_linear_simt(const LinearGemm& g, const DeviceInfo&, cudaStream_t s) {
+  const int64_t mt = (g.M + kSimtBt - 1) / kSimtBt, jt = (g.J + kSimtBt - 1) / kSimtBt;
+  if (mt * jt > 0x7fffffffll) return -1;
+  const dim3 grid(static_cast<unsigned>(mt * jt));
+  if (g.a_mn && g.b_mn)
+    linear_simt_kernel<true, true><<<grid, 256, 0, s>>>(g, mt);
+  else if (g.a_mn)
+    linear_simt_kernel<true, false><<<grid, 256, 0, s>>>(g, mt);
+  else
+    linear_simt_kernel<false, false><<<grid, 256, 0, s>>>(g, mt);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
-template int launch_linear_simt<float>(const LinearGemm&, const DeviceInfo&, cudaStream_t);
-template int launch_linear_simt<__nv_bfloat16>(const LinearGemm&, const DeviceInfo&, cudaStream_t);
 
 int col_sum_blocks(int d_out) { return (d_out + 31) / 32; }
 
@@ -490,21 +488,41 @@ template int launch_moe_route<__nv_bfloat16>(const MoeShape&, const __nv_bfloat1
 template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
                             const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
-                            float* part, int* status, cudaStream_t s) {
-  moe_expert_kernel<T, 0><<<dim3((m.f + 7) / 8, m.experts), 256, 0, s>>>(
-      m, X, ids, Wgu, hidden, nullptr, N, m.act, status);
-  moe_expert_kernel<T, 1><<<dim3((m.d + 7) / 8, m.experts), 256, 0, s>>>(
-      m, hidden, ids, Wd, nullptr, part, N, m.act, status);
-  moe_combine_kernel<T><<<dim3((m.d + 255) / 256, N), 256, 0, s>>>(m, ids, weights, part, residual,
-                                                                   Y, N, status);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+                            float* part, int* status, cudaStream_t s, bool pdl) {
+  const bool vec = m.d * sizeof(T) % 16 == 0 && m.f * sizeof(T) % 16 == 0;
+  auto up = vec ? moe_expert_kernel<T, 0, true> : moe_expert_kernel<T, 0, false>;
+  auto down = vec ? moe_expert_kernel<T, 1, true> : moe_expert_kernel<T, 1, false>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.gridDim = dim3((m.f + 7) / 8, m.experts);
+  cfg.numAttrs = pdl ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, up, m, X, ids, Wgu, hidden, static_cast<float*>(nullptr), N,
+                         status) != cudaSuccess)
+    return -1;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((m.d + 7) / 8, m.experts);
+  if (cudaLaunchKernelEx(&cfg, down, m, static_cast<const T*>(hidden), ids, Wd,
+                         static_cast<T*>(nullptr), part, N, status) != cudaSuccess)
+    return -1;
+  cfg.gridDim = dim3((m.d + 255) / 256, N);
+  return cudaLaunchKernelEx(&cfg, moe_combine_kernel<T>, m, ids, weights,
+                            static_cast<const float*>(part), residual, Y, N,
+                            status) == cudaSuccess
+             ? 0
+             : -1;
 }
 template int launch_moe_experts_simt<float>(const MoeShape&, const float*, const int*,
                                             const float*, const float*, const float*, const float*,
-                                            float*, int, float*, float*, int*, cudaStream_t);
+                                            float*, int, float*, float*, int*, cudaStream_t,
+                                            bool);
 template int launch_moe_experts_simt<__nv_bfloat16>(
     const MoeShape&, const __nv_bfloat16*, const int*, const float*, const __nv_bfloat16*,
     const __nv_bfloat16*, const __nv_bfloat16*, __nv_bfloat16*, int, __nv_bfloat16*, float*, int*,
-    cudaStream_t);
+    cudaStream_t, bool);
 
 }  // namespace dyra
