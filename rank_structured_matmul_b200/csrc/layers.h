@@ -28,6 +28,8 @@ struct LinearGemm {
   void* Out = nullptr;
   void* Z = nullptr;
   int* status = nullptr;
+  float* ws = nullptr;      // tensor cores: linear_ws_bytes of scratch
+  int* counters = nullptr;  // tensor cores: linear_counters ints, zero between calls
 };
 
 // CUDA-core products: fp32 (layers_f32.cu), and bf16 for DYRA_KERNELS=simt
@@ -38,6 +40,8 @@ int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t 
 // Tensor-core product of bf16 operands (layers_umma.cu). pdl: a programmatic
 // dependent launch behind the grid before it in the stream.
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl);
+size_t linear_ws_bytes(const DeviceInfo& dev);
+int linear_counters(const DeviceInfo& dev);
 
 // dZ = dY act'(Z) (skipped for DYRA_ACT_NONE) and its column sums (skipped
 // when dbias is NULL). partial: kColSumChunks x d_out floats; counters:

@@ -21,6 +21,9 @@ struct dyra_dense {
   bool simt = false;        // fp32, or DYRA_KERNELS=simt (debugging)
   float* colsum = nullptr;  // kColSumChunks x d_out partial column sums
   int* counters = nullptr;  // col_sum_blocks(d_out) arrival counters, zero between calls
+  float* ws = nullptr;      // tensor cores: parts of split tiles, and
+  int* tiles = nullptr;     // their arrival counters, zero between calls
+  int n_tiles = 0;
   int* status = nullptr;
   size_t bytes = 0;
 };
@@ -111,6 +114,8 @@ int act_backward(const dyra_dense* p, const void* dY, const void* Z, int act, vo
 void dense_free(dyra_dense* p) {
   give(p->colsum);
   give(p->counters);
+  give(p->ws);
+  give(p->tiles);
   give(p->status);
   delete p;
 }
@@ -203,9 +208,12 @@ int dyra_dense_create(dyra_dense_t* out, int d_in, int d_out, dyra_dtype_t dtype
   p->dtype = dtype;
   p->dev = dev;
   p->simt = dtype == DYRA_F32 || simt_requested();
+  p->n_tiles = p->simt ? 0 : linear_counters(dev);
   if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
       (rc = take(&p->colsum, sizeof(float) * kColSumChunks * d_out, &p->bytes)) ||
-      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes))) {
+      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes)) ||
+      (!p->simt && (rc = take(&p->ws, linear_ws_bytes(dev), &p->bytes))) ||
+      (!p->simt && (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes)))) {
     dense_free(p);
     return rc;
   }
@@ -236,6 +244,8 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   g.Out = Y;
   g.Z = Z;
   g.status = p->status;
+  g.ws = p->ws;
+  g.counters = p->tiles;
   return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream), false));
 }
 
@@ -268,6 +278,8 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
   }
   LinearGemm g;
   g.status = p->status;
+  g.ws = p->ws;
+  g.counters = p->tiles;
   g.B = has_act ? dZ : dY;
   g.M = p->d_in;
   if (dX) {
@@ -292,7 +304,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
 }
 
 int dyra_dense_status(dyra_dense_t p) {
-  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status, nullptr, 0);
+  return p == nullptr ? DYRA_ERR_INVALID_ARG : read_status(p->dev, p->status, p->tiles, p->n_tiles);
 }
 
 size_t dyra_dense_device_bytes(dyra_dense_t p) { return p == nullptr ? 0 : p->bytes; }

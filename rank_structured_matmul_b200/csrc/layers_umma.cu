@@ -48,6 +48,13 @@ struct DensePairParams {
   int act;
   const __nv_bfloat16* bias;
   const __nv_bfloat16* residual;
+  // The first `whole` tiles are a pair's each; of the `tail` others each is split
+  // over its steps between `split` pairs, which leave their fp32 parts in ws
+  // ([tail tile][part][CTA of the pair][column / 4][128 rows] float4s); the last
+  // CTA to arrive of each half tile sums them in order.
+  int whole, tail, split;
+  float* ws;
+  int* counters;  // two per tail tile, zero between calls
 };
 
 // What a pair kernel is compiled with: the gradients' products store the
@@ -56,13 +63,15 @@ struct DensePairParams {
 // residual that comes by TMA into the store boxes.
 enum PairEpilogue { kPlain, kForward, kForwardZ, kForwardResidual };
 
-template <bool kRowMn, bool kColMn, PairEpilogue kMode>
+// kTail: some tiles are split between pairs (Params::split > 1).
+template <bool kRowMn, bool kColMn, PairEpilogue kMode, bool kTail>
 struct DensePairPolicy {
   static constexpr bool kEpi = kMode != kPlain, kKeepZ = kMode == kForwardZ,
                         kTmaRes = kMode == kForwardResidual;
   using Params = DensePairParams;
   struct Tile {
-    int j0, m0;
+    int j0, m0, k0, nk;
+    int tail, part;  // tail < 0: a whole tile; nk == 0: nothing
   };
   // Two groups of four epilogue warps take the tile's 64-column boxes in turn,
   // each with a store box of its own (two with Z or a residual): a tile of
@@ -71,7 +80,7 @@ struct DensePairPolicy {
   static constexpr int kEpiWarps = 8;
   static constexpr int kMaxRegs = 200;  // 320 threads
   static constexpr uint32_t kGroupBytes = (kKeepZ || kTmaRes ? 2 : 1) * kStoreBoxBytes;
-  static constexpr uint32_t kEpiSmemBytes = 2 * kGroupBytes + (kTmaRes ? 64 : 0);
+  static constexpr uint32_t kEpiSmemBytes = 2 * kGroupBytes + 64;  // barriers, a word
 
   static __device__ __forceinline__ void prefetch(const Params& p) {
     tma_prefetch_desc(&p.tmRow);
@@ -79,14 +88,25 @@ struct DensePairPolicy {
     tma_prefetch_desc(&p.tmOut);
   }
   static __device__ __forceinline__ void decode(const Params& p, int tile, Tile& t) {
+    const int steps = ceil_div_dev(p.K, 64);
+    t.k0 = 0;
+    t.nk = steps;
+    t.tail = -1;
+    t.part = 0;
+    if (kTail && tile >= p.whole) {
+      t.tail = (tile - p.whole) / p.split;
+      t.part = (tile - p.whole) - t.tail * p.split;
+      t.k0 = t.part * steps / p.split;
+      t.nk = (t.part + 1) * steps / p.split - t.k0;
+      tile = p.whole + t.tail;
+    }
     t.j0 = (tile / p.tiles_m) * 256;
     t.m0 = (tile % p.tiles_m) * p.bn;
   }
-  static __device__ __forceinline__ int kiters(const Params& p, const Tile&) {
-    return ceil_div_dev(p.K, 64);
-  }
+  static __device__ __forceinline__ int kiters(const Params&, const Tile& t) { return t.nk; }
   static __device__ __forceinline__ void load(const Params& p, const Tile& t, int it, uint32_t sa,
                                               uint32_t sb, uint32_t bar, uint32_t rank) {
+    it += t.k0;
     const int j = t.j0 + 128 * static_cast<int>(rank);
     const int m = t.m0 + (p.bn / 2) * static_cast<int>(rank);
     if (kRowMn) {
@@ -102,8 +122,8 @@ struct DensePairPolicy {
       tma_load_2d_pair(sb, &p.tmCol, bar, it * 64, m);
     }
   }
-  static __device__ __forceinline__ int ksteps(const Params& p, const Tile&, int it) {
-    return min(4, ceil_div_dev(p.K - it * 64, 16));
+  static __device__ __forceinline__ int ksteps(const Params& p, const Tile& t, int it) {
+    return min(4, ceil_div_dev(p.K - (t.k0 + it) * 64, 16));
   }
   static __device__ __forceinline__ uint64_t adesc(const Params&, uint32_t a, int ks) {
     return kRowMn ? mnmajor_desc(a, ks) : kmajor_desc(a, ks);
@@ -112,12 +132,9 @@ struct DensePairPolicy {
     return kColMn ? mnmajor_desc(b, ks) : kmajor_desc(b, ks);
   }
 
-  // 16 values of this thread's row as the 16-byte chunks c, c + 1 of a 64-column
-  // store box (128-byte swizzle)
-  static __device__ __forceinline__ void put2(uint8_t* box, int row, int c, const float (&v)[16]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<uint4*>(box + row * 128 + (((c + h) ^ (row & 7)) * 16)) = pack8(v + 8 * h);
+  // 16-byte chunk c of this thread's row in a 64-column store box (128-byte swizzle)
+  static __device__ __forceinline__ uint4* chunk(uint8_t* box, int row, int c) {
+    return reinterpret_cast<uint4*>(box + row * 128 + ((c ^ (row & 7)) * 16));
   }
   // A half box's residual: 8 columns per load, all inside or all beyond M.
   struct Residual {
@@ -133,10 +150,72 @@ struct DensePairPolicy {
         r.q[c] = *reinterpret_cast<const uint4*>(p.residual + at + c * 8);
     }
   }
+  static __device__ __forceinline__ float4* part_of(const Params& p, const Tile& t, int part,
+                                                    int rank) {
+    return reinterpret_cast<float4*>(p.ws) +
+           (static_cast<size_t>(t.tail * p.split + part) * 2 + rank) * (p.bn / 4) * 128;
+  }
+  // A tail tile's part into the workspace; true where it is the last to arrive.
+  static __device__ __forceinline__ bool leave_part(const Params& p, const Tile& t, uint32_t tacc,
+                                                    EpiCtx& e) {
+    float4* part = part_of(p, t, t.part, e.rank);
+    for (int c = e.group * 32; c < p.bn; c += 64) {
+      __syncwarp();
+      uint32_t raw[32];
+      tmem_ld_32x32b_x32(tacc + c, raw);
+      tmem_ld_wait();
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        part[(c / 4 + q) * 128 + e.row] = make_float4(f32(raw[4 * q]), f32(raw[4 * q + 1]),
+                                                      f32(raw[4 * q + 2]), f32(raw[4 * q + 3]));
+    }
+    volatile int* last = reinterpret_cast<volatile int*>(e.smem + 2 * kGroupBytes + 48);
+    __threadfence();
+    named_bar_sync(3, 256);
+    if (e.group == 0 && e.tid == 0) {
+      int* counter = p.counters + 2 * t.tail + e.rank;
+      const int old = atomicAdd(counter, 1);
+      if (old == p.split - 1) *counter = 0;
+      *last = old == p.split - 1;
+    }
+    named_bar_sync(3, 256);
+    const bool is_last = *last != 0;
+    named_bar_sync(3, 256);  // the word may be written again
+    if (is_last) __threadfence();
+    return is_last;
+  }
+  // raw = the sum of the parts' columns col .. col + 31 of this row, in order
+  static __device__ __forceinline__ void sum_parts(const Params& p, const Tile& t, int col,
+                                                   const EpiCtx& e, uint32_t (&raw)[32]) {
+    float v[32] = {};
+    for (int part = 0; part < p.split; part += 2) {
+      const float4* a = part_of(p, t, part, e.rank) + (col / 4) * 128 + e.row;
+      const float4* b = part_of(p, t, min(part + 1, p.split - 1), e.rank) + (col / 4) * 128 + e.row;
+      float4 x[8], y[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        x[q] = __ldcg(a + q * 128);
+        y[q] = __ldcg(b + q * 128);
+      }
+      const float two = part + 1 < p.split ? 1.f : 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        v[4 * q] += x[q].x, v[4 * q + 1] += x[q].y, v[4 * q + 2] += x[q].z, v[4 * q + 3] += x[q].w;
+        if (two != 0.f) {
+          v[4 * q] += y[q].x, v[4 * q + 1] += y[q].y, v[4 * q + 2] += y[q].z;
+          v[4 * q + 3] += y[q].w;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) raw[j] = __float_as_uint(v[j]);
+  }
   // Half boxes of 32 columns, one at a time (straight-line code for a whole box
   // outgrows the instruction cache), the next one's residual in flight.
   static __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, uint32_t tacc,
                                                   EpiCtx& e) {
+    const bool summed = kTail && t.tail >= 0;
+    if (summed && !leave_part(p, t, tacc, e)) return;
     const int y0 = t.j0 + 128 * e.rank, row = y0 + e.row;
     const int nbox = min(p.bn, p.M - t.m0 + 63) / 64;
     uint8_t* const box = e.smem + e.group * kGroupBytes;
@@ -170,7 +249,10 @@ struct DensePairPolicy {
       uint8_t* const dst = box + (kTmaRes ? (e.counter & 1) * kStoreBoxBytes : 0u);
       __syncwarp();
       uint32_t raw[32];
-      tmem_ld_32x32b_x32(tacc + col, raw);
+      if (summed)
+        sum_parts(p, t, col, e, raw);
+      else
+        tmem_ld_32x32b_x32(tacc + col, raw);
       uint4 bq[4];
       if (kEpi && p.bias) {
 #pragma unroll
@@ -189,10 +271,7 @@ struct DensePairPolicy {
           atomicOr(p.c.status, kStatusTimeout);
       }
       tmem_ld_wait();
-      if (!kTmaRes && !half) {  // the box is free once its last store has been read
-        if (e.tid == 0) tma_store_wait_read<0>();
-        named_bar_sync(bar, 128);
-      }
+      uint4 y[4], z[4];
 #pragma unroll
       for (int c = 0; c < 4; c += 2) {
         float v[16];
@@ -203,7 +282,7 @@ struct DensePairPolicy {
             add8(v, bq[c]);
             add8(v + 8, bq[c + 1]);
           }
-          if (kKeepZ) put2(box + kStoreBoxBytes, e.row, half * 4 + c, v);
+          if (kKeepZ) z[c] = pack8(v), z[c + 1] = pack8(v + 8);
           // the branch on the activation sits here: around the whole loop it
           // costs the registers of five loops
           with_act(p.act, [&](auto tag) {
@@ -211,17 +290,24 @@ struct DensePairPolicy {
             for (int j = 0; j < 16; ++j) v[j] = act_f<decltype(tag)::value, true>(v[j]);
           });
           if (kTmaRes) {  // the residual's chunks lie where the result's will
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              add8(v + 8 * h, *reinterpret_cast<const uint4*>(
-                                  dst + e.row * 128 + (((half * 4 + c + h) ^ (e.row & 7)) * 16)));
+            add8(v, *chunk(dst, e.row, half * 4 + c));
+            add8(v + 8, *chunk(dst, e.row, half * 4 + c + 1));
           }
           if (has_r) {
             add8(v, r.q[c]);
             add8(v + 8, r.q[c + 1]);
           }
         }
-        put2(dst, e.row, half * 4 + c, v);
+        y[c] = pack8(v), y[c + 1] = pack8(v + 8);
+      }
+      if (!kTmaRes && !half) {  // the box is free once its last store has been read
+        if (e.tid == 0) tma_store_wait_read<0>();
+        named_bar_sync(bar, 128);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        *chunk(dst, e.row, half * 4 + c) = y[c];
+        if (kKeepZ) *chunk(box + kStoreBoxBytes, e.row, half * 4 + c) = z[c];
       }
       if (half) {
         fence_async_shared();
@@ -247,9 +333,36 @@ bool encode_2d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, uin
   return encode_tmap_bf16(tm, base, 2, dims, strides, box, 128);
 }
 
-template <bool kRowMn, bool kColMn, PairEpilogue kMode>
-int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  using Pol = DensePairPolicy<kRowMn, kColMn, kMode>;
+// How the tiles go over the pairs: where the last round has few tiles, each is
+// split between several pairs. In nanoseconds: a step of a tile takes 350, its
+// epilogue 2000, and joining s parts 3000 + 1600 s (their way through L2). dW of
+// 12000 rows, 1280 -> 5120, 100 tiles on 74 pairs: 127 us in two rounds, 112 with the last 26 split in two.
+struct PairPlan {
+  int split = 1;
+  double ns = 0.0;
+};
+PairPlan plan_pairs(int64_t tiles, int64_t steps, const DeviceInfo& dev) {
+  const int64_t pairs = dev.sm_count / 2, rounds = tiles / pairs, tail = tiles % pairs;
+  const double tile_ns = 350.0 * static_cast<double>(steps) + 2000.0;
+  PairPlan best;
+  best.ns = 6500.0 + static_cast<double>(rounds + (tail > 0 ? 1 : 0)) * tile_ns;
+  if (tail == 0) return best;
+  for (int s = 2; s <= pairs / tail && s <= 16 && s * 4 <= steps; ++s) {
+    const double ns = 6500.0 + static_cast<double>(rounds) * tile_ns +
+                      350.0 * static_cast<double>((steps + s - 1) / s) + 2000.0 + 3000.0 +
+                      1600.0 * s;
+    if (ns < best.ns) {
+      best.ns = ns;
+      best.split = s;
+    }
+  }
+  return best;
+}
+
+template <bool kRowMn, bool kColMn, PairEpilogue kMode, bool kTail>
+int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaStream_t s,
+                   bool pdl) {
+  using Pol = DensePairPolicy<kRowMn, kColMn, kMode, kTail>;
   DensePairParams p;
   p.J = static_cast<int>(g.J);
   p.M = static_cast<int>(g.M);
@@ -270,12 +383,25 @@ int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool
   if (!ok) return -2;
   const int64_t tiles = static_cast<int64_t>(ceil_div(g.J, 256)) * p.tiles_m;
   if (tiles > 0x7fffffff) return -2;
+  p.split = split;
+  p.tail = split > 1 ? static_cast<int>(tiles % (dev.sm_count / 2)) : 0;
+  p.whole = static_cast<int>(tiles) - p.tail;
+  p.ws = g.ws;
+  p.counters = g.counters;
   const uint32_t smem =
-      setup_common<Pol>(p.c, static_cast<int>(tiles), 128 * 128, (p.bn / 2) * 128, p.bn, kRowMn,
+      setup_common<Pol>(p.c, p.whole + p.tail * p.split, 128 * 128, (p.bn / 2) * 128, p.bn, kRowMn,
                         kColMn, g.status, dev);
   if (!smem) return -3;
   p.c.idesc = idesc_bf16(256, p.bn, kRowMn, kColMn);
   return launch_gemm_pair<Pol>(p, smem, dev, s, pdl);
+}
+
+template <bool kRowMn, bool kColMn, PairEpilogue kMode>
+int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+  const int64_t tiles = static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
+  const int split = plan_pairs(tiles, ceil_div(g.K, 64), dev).split;
+  return split > 1 ? launch_pair_as<kRowMn, kColMn, kMode, true>(g, split, dev, s, pdl)
+                   : launch_pair_as<kRowMn, kColMn, kMode, false>(g, 1, dev, s, pdl);
 }
 
 // --------------------------------------------------------------- clusters ----
@@ -417,8 +543,7 @@ SplitChoice choose_split(const LinearGemm& g, const DeviceInfo& dev) {
       static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
   const int64_t pairs = dev.sm_count / 2;
   SplitChoice best;
-  double best_ns = 6500.0 + static_cast<double>((pair_tiles + pairs - 1) / pairs) *
-                                (350.0 * static_cast<double>(ks) + 2000.0);
+  double best_ns = plan_pairs(pair_tiles, ks, dev).ns;
   if (pair_tiles > 2 * pairs) return best;  // many full tiles
   const int exact = ceil_div(std::min<int64_t>(g.J, kStreamMaxNb), 16) * 16;
   for (int nb : {16, 32, 64, exact, kStreamMaxNb}) {
@@ -442,6 +567,11 @@ SplitChoice choose_split(const LinearGemm& g, const DeviceInfo& dev) {
 }
 
 }  // namespace
+
+size_t linear_ws_bytes(const DeviceInfo& dev) {  // a part of 256 x 256 per pair
+  return static_cast<size_t>(dev.sm_count / 2) * 256 * 256 * sizeof(float);
+}
+int linear_counters(const DeviceInfo& dev) { return dev.sm_count; }
 
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
   const SplitChoice ch = choose_split(g, dev);

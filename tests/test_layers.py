@@ -172,6 +172,51 @@ def test_backward_f32(N, d_in, d_out):
     layer.close()
 
 
+@pytest.mark.parametrize("N,d_in,d_out", [(9700, 1024, 512), (6500, 264, 4096), (2600, 520, 1544)])
+def test_forward_many_tiles(N, d_in, d_out):
+    """More 256 x 256 tiles than pairs of SMs, with a last round of few tiles
+    (76 of 74), of most, and ragged in both directions: every form of the
+    epilogue."""
+    layer = layers.DenseLinear(d_in, d_out, "bf16")
+    X, W, b, R = dense_case(N, d_in, d_out, "bf16")
+    z = X.double() @ W.double().t()
+    mag = X.double().abs() @ W.double().abs().t() + b.double().abs()
+    k, u = (d_in + 8) * 2.0 ** -23, U["bf16"]
+    for act, bias, res, save in (("gelu", b, R, False), ("silu", b, R, True), ("none", None, R, False),
+                                 ("gelu_tanh", b, None, True), ("relu", b, None, False),
+                                 ("none", None, None, False)):
+        zb = z if bias is None else z + b.double()
+        y = act64(zb, act)
+        tol = u * y.abs() + 1.2 * k * mag + 2.0 ** -20 * zb.abs()
+        if res is not None:
+            y = y + R.double()
+            tol = tol + u * y.abs() + 2.0 ** -23 * (y.abs() + R.double().abs())
+        out = layer.forward(X, W, bias=bias, residual=res, act=act, save_z=save)
+        Y, Z = out if save else (out, None)
+        assert_within(Y, y, tol, "Y %s" % act)
+        if save:
+            assert_within(Z, zb, u * zb.abs() + k * mag, "Z")
+        again = layer.forward(X, W, bias=bias, residual=res, act=act)
+        assert torch.equal(again, Y)
+    got = R.clone()
+    layer.forward(X, W, bias=b, residual=got, act="gelu", Y=got)
+    assert torch.equal(got, layer.forward(X, W, bias=b, residual=R, act="gelu"))
+    assert layer.status() == 0
+    layer.close()
+
+
+@pytest.mark.parametrize("N,d_in,d_out", [(9700, 512, 4096), (6000, 1280, 5120), (12345, 264, 136)])
+def test_backward_many_rows(N, d_in, d_out):
+    """Long sums and last rounds of few tiles (dX of 76 tiles, dW of 100)."""
+    layer = layers.DenseLinear(d_in, d_out, "bf16")
+    X, W, b, R = dense_case(N, d_in, d_out, "bf16")
+    _, Z = layer.forward(X, W, bias=b, act="gelu", save_z=True)
+    first = check_backward(layer, X, W, Z, R, "gelu", "bf16")
+    for a, c in zip(first, layer.backward(R, X, W, Z=Z, act="gelu")):
+        assert torch.equal(a, c)
+    layer.close()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("act", ACTS)
 def test_backward_activations(act, dtype):
