@@ -99,7 +99,8 @@ int dyra_dense_destroy(dyra_dense_t p);
 /*
  * A mixture-of-experts layer: `experts` gated MLPs of d_model -> d_ff ->
  * d_model, of which each token uses top_k.
- *   d_model, d_ff >= 1 (multiples of 8 for DYRA_BF16, else DYRA_ERR_ALIGNMENT)
+ *   1 <= d_model, d_ff <= DYRA_MOE_MAX_WIDTH (multiples of 8 for DYRA_BF16, else
+ *   DYRA_ERR_ALIGNMENT)
  *   1 <= top_k <= experts, top_k <= DYRA_MOE_MAX_TOP_K, experts <= DYRA_MOE_MAX_EXPERTS
  *   act    : DYRA_ACT_*, the activation of the gate
  *   renorm : 1: a token's weights are the softmax over its top_k logits (they
@@ -110,6 +111,7 @@ int dyra_dense_destroy(dyra_dense_t p);
  */
 #define DYRA_MOE_MAX_TOP_K 16
 #define DYRA_MOE_MAX_EXPERTS 512
+#define DYRA_MOE_MAX_WIDTH (1 << 20)
 int dyra_moe_create(dyra_moe_t *out, int d_model, int d_ff, int experts, int top_k, int act,
                     int renorm, dyra_dtype_t dtype);
 

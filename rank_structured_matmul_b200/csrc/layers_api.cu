@@ -321,7 +321,8 @@ int dyra_moe_create(dyra_moe_t* out, int d_model, int d_ff, int experts, int top
                     int renorm, dyra_dtype_t dtype) {
   if (out == nullptr) return DYRA_ERR_INVALID_ARG;
   if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_ERR_INVALID_ARG;
-  if (d_model < 1 || d_ff < 1 || d_ff > (1 << 29) || experts < 1 ||
+  if (d_model < 1 || d_ff < 1 || d_model > DYRA_MOE_MAX_WIDTH || d_ff > DYRA_MOE_MAX_WIDTH ||
+      experts < 1 ||
       experts > DYRA_MOE_MAX_EXPERTS || top_k < 1 || top_k > DYRA_MOE_MAX_TOP_K ||
       top_k > experts || !known_act(act) || (renorm != 0 && renorm != 1))
     return DYRA_ERR_INVALID_ARG;

@@ -488,7 +488,8 @@ def check_experts(layer, X, ids, w, Wgu, Wd, R, act, dtype):
 
 MOE_BF16 = [(1, 64, 64, 4, 1), (1, 512, 1024, 8, 2), (2, 128, 72, 8, 8), (3, 1000, 488, 17, 3),
             (7, 136, 200, 64, 4), (16, 256, 512, 8, 2), (17, 264, 136, 5, 2), (33, 2048, 128, 9, 3),
-            (64, 512, 256, 128, 8), (64, 8, 8, 3, 3), (1, 4096, 2048, 2, 2), (48, 72, 1032, 300, 16)]
+            (64, 512, 256, 128, 8), (64, 8, 8, 3, 3), (1, 4096, 2048, 2, 2), (48, 72, 1032, 300, 16),
+            (33, 16, 24, 512, 16), (5, 1288, 8, 3, 1), (40, 8, 2056, 2, 2)]
 MOE_F32 = [(1, 1, 1, 1, 1), (3, 256, 512, 8, 2), (5, 33, 17, 6, 3), (64, 65, 70, 12, 4),
            (2, 1000, 251, 4, 2)]
 
@@ -619,6 +620,26 @@ def test_moe_more_than_one_group(dtype):
     assert_within(one, y, tol, "one token of the group")
     e = torch.empty(0, d, device="cuda", dtype=DT[dtype])
     assert layer.forward(e, Wr, Wgu, Wd)[0].shape == (0, d)
+    layer.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_route_many_tokens(dtype):
+    """More tokens than one launch of the router takes."""
+    N, d, E, K = 2100, 72, 37, 5
+    layer = layers.MoeLayer(d, 8, E, K, dtype, renorm=False)
+    g = gen(4)
+    X, Wr = rand(g, N, d, dtype=dtype), rand(g, E, d, dtype=dtype, scale=d ** -0.5)
+    ids, w = layer.route(X, Wr)
+    logits = X.double() @ Wr.double().t()
+    order = torch.sort(logits, dim=1, descending=True, stable=True)
+    gap = (order.values[:, :K] - logits.gather(1, ids.long())).abs()
+    assert (gap <= 2.0 ** -20 * (X.double().abs() @ Wr.double().abs().t()).amax(1, True)).all()
+    w64 = torch.softmax(logits, 1).gather(1, ids.long())
+    assert ((w.double() - w64).abs() <= (E + 8) * 2.0 ** -23 * w64 + 4 * 2.0 ** -20 * w64).all()
+    part, wp = layer.route(X[1500:1510].clone(), Wr)
+    assert torch.equal(part, ids[1500:1510]) and torch.equal(wp, w[1500:1510])
+    assert layer.status() == 0
     layer.close()
 
 

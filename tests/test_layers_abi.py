@@ -28,6 +28,8 @@ def test_dense_create_rejects(args, code):
 @pytest.mark.parametrize("args,code", [
     ((0, 64, 8, 2, 4, 1, F32), INV),     # d_model < 1
     ((64, 0, 8, 2, 4, 1, F32), INV),     # d_ff < 1
+    ((2 ** 20 + 8, 64, 8, 2, 4, 1, F32), INV),  # d_model > 2^20
+    ((64, 2 ** 20 + 8, 8, 2, 4, 1, BF16), INV),
     ((64, 64, 0, 1, 4, 1, F32), INV),    # experts < 1
     ((64, 64, 513, 2, 4, 1, F32), INV),  # experts > 512
     ((64, 64, 8, 0, 4, 1, F32), INV),    # top_k < 1
