@@ -334,23 +334,29 @@ bool encode_2d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, uin
 }
 
 // How the tiles go over the pairs: where the last round has few tiles, each is
-// split between several pairs. In nanoseconds: a step of a tile takes 350, its
-// epilogue 2000, and joining s parts 3000 + 1600 s (their way through L2). dW of
-// 12000 rows, 1280 -> 5120, 100 tiles on 74 pairs: 127 us in two rounds, 112 with the last 26 split in two.
+// split between several pairs. In nanoseconds: a step of a tile takes 310 and a
+// tile's epilogue 1500 beside it, starting and ending 8500 for the forward with its
+// activation, 7000 for dX, 4500 for dW, and joining s parts 3000 + 1600 s (their way
+// through L2). dW of 12000 rows, 1280 -> 5120, 100 tiles on 74 pairs: 127 us in two
+// rounds, 112 with the last 26 tiles split in two.
 struct PairPlan {
   int split = 1;
   double ns = 0.0;
 };
-PairPlan plan_pairs(int64_t tiles, int64_t steps, const DeviceInfo& dev) {
+PairPlan plan_pairs(const LinearGemm& g, const DeviceInfo& dev) {
+  const int64_t tiles =
+      static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
+  const int64_t steps = ceil_div(g.K, 64);
   const int64_t pairs = dev.sm_count / 2, rounds = tiles / pairs, tail = tiles % pairs;
-  const double tile_ns = 350.0 * static_cast<double>(steps) + 2000.0;
+  const double tile_ns = 310.0 * static_cast<double>(steps) + 1500.0;
+  const double base = (g.b_mn ? 4500.0 : g.a_mn ? 7000.0 : 8500.0) +
+                      static_cast<double>(rounds) * tile_ns;
   PairPlan best;
-  best.ns = 6500.0 + static_cast<double>(rounds + (tail > 0 ? 1 : 0)) * tile_ns;
+  best.ns = base + (tail > 0 ? tile_ns : 0.0);
   if (tail == 0) return best;
   for (int s = 2; s <= pairs / tail && s <= 16 && s * 4 <= steps; ++s) {
-    const double ns = 6500.0 + static_cast<double>(rounds) * tile_ns +
-                      350.0 * static_cast<double>((steps + s - 1) / s) + 2000.0 + 3000.0 +
-                      1600.0 * s;
+    const double ns =
+        base + 310.0 * static_cast<double>((steps + s - 1) / s) + 4500.0 + 1600.0 * s;
     if (ns < best.ns) {
       best.ns = ns;
       best.split = s;
@@ -398,8 +404,7 @@ int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaSt
 
 template <bool kRowMn, bool kColMn, PairEpilogue kMode>
 int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
-  const int64_t tiles = static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
-  const int split = plan_pairs(tiles, ceil_div(g.K, 64), dev).split;
+  const int split = plan_pairs(g, dev).split;
   return split > 1 ? launch_pair_as<kRowMn, kColMn, kMode, true>(g, split, dev, s, pdl)
                    : launch_pair_as<kRowMn, kColMn, kMode, false>(g, 1, dev, s, pdl);
 }
@@ -529,33 +534,30 @@ int resident_clusters(int cs, const DeviceInfo& dev) {
   return n;
 }
 
-// CTA pairs or clusters, by a model of both in nanoseconds, fitted to 4096 ->
-// 14336, 1280 -> 5120, 4096 -> 1024, 1024 -> 1024 and 1024 -> 4096 at 1 to 1024
-// rows (cold weights). A pair's step of 256 x 256 x 64 takes 350 whatever part of
-// the tile exists; a cluster CTA's step takes its 16 KB of A and nb rows of B at
-// 75 bytes per ns, and finishing a tile costs its columns. 64 rows through 1024 ->
-// 1024: 6.2 us in clusters of 4, 15.3 on pairs; 512 rows through 4096 -> 14336: 57
-// on pairs, 105 in clusters.
+// CTA pairs or clusters, by a model of both in nanoseconds (plan_pairs; below), a
+// least-squares fit over the forward, dX and dW of nine shapes from 104 -> 96 to 4096
+// -> 14336 at 1 to 3000 rows with cold weights. Over those its choice is 1% slower
+// than the fastest on average, 15% at worst. 64 rows through 1024 -> 1024: 6.9 us in
+// clusters of 4, 15.3 on pairs; 450 rows through 4096 -> 14336: 56 on pairs, 105 in
+// clusters.
 SplitChoice choose_split(const LinearGemm& g, const DeviceInfo& dev) {
   const int64_t ks = ceil_div(g.K, 64), tm = ceil_div(g.M, 128);
-  const double weights_ns = 2.0 * static_cast<double>(g.M) * g.K / 5200.0;
-  const int64_t pair_tiles =
-      static_cast<int64_t>(ceil_div(g.J, 256)) * ceil_div(g.M, g.M > 128 ? 256 : 128);
-  const int64_t pairs = dev.sm_count / 2;
+  const double weights_ns = 2.0 * static_cast<double>(g.M) * static_cast<double>(g.K) / 5200.0;
   SplitChoice best;
-  double best_ns = plan_pairs(pair_tiles, ks, dev).ns;
-  if (pair_tiles > 2 * pairs) return best;  // many full tiles
-  const int exact = ceil_div(std::min<int64_t>(g.J, kStreamMaxNb), 16) * 16;
-  for (int nb : {16, 32, 64, exact, kStreamMaxNb}) {
-    if (nb > exact && !(g.b_mn && nb == 64)) continue;
-    if (g.b_mn && nb % 64) continue;  // whole boxes of 64
+  double best_ns = plan_pairs(g, dev).ns;
+  const int64_t most = std::min<int64_t>(kStreamMaxNb, (g.J + 15) / 16 * 16);
+  const int unit = g.b_mn ? 64 : 16;  // an MN-major operand comes in whole boxes of 64
+  for (int nb = unit; nb <= std::max<int64_t>(most, unit); nb += unit) {
     const int64_t tiles = tm * ceil_div(g.J, nb);
     if (tiles > 4 * dev.sm_count) continue;
-    for (int cs = 1; cs <= 8 && cs <= ks; ++cs) {
-      const int64_t waves = (tiles + resident_clusters(cs, dev) - 1) / resident_clusters(cs, dev);
-      const double cta_ns = static_cast<double>(ceil_div(ks, cs)) * (16384 + 128 * nb) / 75.0 +
-                            30.0 * nb / cs + 10.0 * nb + 100.0 * cs;
-      const double ns = 4500.0 + std::max(static_cast<double>(waves) * cta_ns, weights_ns);
+    const double n = static_cast<double>(std::min<int64_t>(nb, g.J));
+    for (int cs : {1, 2, 3, 4, 6, 8}) {
+      if (cs > ks) break;
+      const int resident = resident_clusters(cs, dev);
+      const double waves = static_cast<double>((tiles + resident - 1) / resident);
+      const double cta_ns = 227.0 * static_cast<double>((ks + cs - 1) / cs) - 48.0 * n +
+                            109.0 * n / cs + (cs > 1 ? (147.0 + 14.4 * n) * cs - 673.0 : 0.0);
+      const double ns = 5550.0 + std::max(waves * cta_ns + (waves - 1.0) * 4000.0, weights_ns);
       if (ns < best_ns) {
         best_ns = ns;
         best.nb = nb;
@@ -575,6 +577,7 @@ int linear_counters(const DeviceInfo& dev) { return dev.sm_count; }
 
 int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
   const SplitChoice ch = choose_split(g, dev);
+
   if (g.a_mn && g.b_mn)
     return ch.nb ? launch_split<true, true, false>(g, ch, dev, s, pdl)
                  : launch_pair<true, true, kPlain>(g, dev, s, pdl);
