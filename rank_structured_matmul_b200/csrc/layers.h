@@ -11,6 +11,32 @@
 
 namespace dyra {
 
+// Every kernel of the layers is a programmatic dependent launch: its grid may be
+// set up while the one before it in the stream still runs, whichever kernel that
+// is, and waits for it (griddepcontrol.wait) before it reads or writes memory. The
+// wait is for the whole grid before, which waited for its own predecessor, so the
+// order of the stream holds. Calls that follow one another hide their launches
+// behind each other in this way.
+template <class Kernel, class... Args>
+inline int launch_dependent(Kernel kfn, dim3 grid, dim3 block, uint32_t smem, int cluster,
+                            cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kfn, args...) == cudaSuccess ? 0 : -1;
+}
+
 // One matrix product with its epilogue, in the form all of the dense layer's
 // products share:
 //   Z[j][m] = sum_k A(m, k) B(j, k) + bias[m],  Out[j][m] = act(Z) + residual[j][m]
@@ -37,9 +63,8 @@ struct LinearGemm {
 int launch_linear_f32(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 int launch_linear_simt(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 
-// Tensor-core product of bf16 operands (layers_umma.cu). pdl: a programmatic
-// dependent launch behind the grid before it in the stream.
-int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl);
+// Tensor-core product of bf16 operands (layers_umma.cu).
+int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s);
 size_t linear_ws_bytes(const DeviceInfo& dev);
 int linear_counters(const DeviceInfo& dev);
 
@@ -70,16 +95,21 @@ template <typename T>
 int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float* weights,
                      int64_t N, double* logits, int* counters, cudaStream_t s);
 
+// The experts' two products in fp32 (layers_f32.cu): hidden, then part.
+int launch_moe_tiles_f32(const MoeShape& m, const float* X, const int* ids, const float* Wgu,
+                         const float* Wd, int N, float* hidden, float* part, int* status,
+                         const DeviceInfo& dev, cudaStream_t s);
+
 // CUDA-core experts for N <= kMoeTokens tokens. hidden: N * top_k x f values,
 // part: N * top_k x d floats.
 template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
                             const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
-                            float* part, int* status, cudaStream_t s, bool pdl);
+                            float* part, int* status, const DeviceInfo& dev, cudaStream_t s);
 
 // Tensor-core experts for N <= kMoeTokens tokens (layers_moe_umma.cu). hidden:
 // moe_reached_max x kMoeTokens x f values; ws and counters (zero between calls)
-// as the sizes below. pdl: launched behind the router's grid.
+// as the sizes below.
 int moe_reached_max(const MoeShape& m);
 int moe_counters(const MoeShape& m);
 size_t moe_ws_bytes(const MoeShape& m, const DeviceInfo& dev);
@@ -87,7 +117,6 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
                             const float* weights, const __nv_bfloat16* Wgu,
                             const __nv_bfloat16* Wd, const __nv_bfloat16* residual,
                             __nv_bfloat16* Y, int N, __nv_bfloat16* hidden, float* ws,
-                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s,
-                            bool pdl);
+                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace dyra

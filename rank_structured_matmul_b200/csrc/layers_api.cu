@@ -97,10 +97,10 @@ int launched(int rc) {
   return DYRA_ERR_CUDA;
 }
 
-int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s, bool pdl) {
+int linear(const dyra_dense* p, const LinearGemm& g, cudaStream_t s) {
   if (p->dtype == DYRA_F32) return launch_linear_f32(g, p->dev, s);
   if (p->simt) return launch_linear_simt(g, p->dev, s);
-  return launch_linear_umma(g, p->dev, s, pdl);
+  return launch_linear_umma(g, p->dev, s);
 }
 
 template <class T>
@@ -138,19 +138,18 @@ int moe_route(const dyra_moe* p, const void* X, const void* Wr, int32_t* ids, fl
 
 template <class T>
 int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const float* weights,
-                const void* Wgu, const void* Wd, const void* residual, void* Y, int n, bool pdl,
-                cudaStream_t s) {
+                const void* Wgu, const void* Wd, const void* residual, void* Y, int n, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
     if (!p->simt)
       return launch_moe_experts_umma(p->m, static_cast<const T*>(X), ids, weights,
                                      static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                      static_cast<const T*>(residual), static_cast<T*>(Y), n,
                                      static_cast<T*>(p->hidden), p->part,
-                                     p->tiles + moe_route_counters(), p->status, p->dev, s, pdl);
+                                     p->tiles + moe_route_counters(), p->status, p->dev, s);
   return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
-                                    static_cast<T*>(p->hidden), p->part, p->status, s, pdl);
+                                    static_cast<T*>(p->hidden), p->part, p->status, p->dev, s);
 }
 
 // The shared checks of the calls on N tokens: DYRA_OK to go on.
@@ -159,10 +158,9 @@ int moe_check(const dyra_moe* p, int64_t N) {
   return DYRA_OK;
 }
 
-// after_route: the router's grid is the one before in the stream.
 int run_experts(const dyra_moe* p, const void* X, const int32_t* ids, const float* weights,
                 const void* Wgu, const void* Wd, const void* residual, void* Y, int64_t N,
-                bool after_route, cudaStream_t s) {
+                cudaStream_t s) {
   int rc = moe_check(p, N);
   if (rc || N == 0) return rc;
   if (X == nullptr || ids == nullptr || weights == nullptr || Wgu == nullptr || Wd == nullptr ||
@@ -178,13 +176,12 @@ int run_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
     const int n = static_cast<int>(std::min<int64_t>(kMoeTokens, N - n0));
     const void* x = static_cast<const char*>(X) + n0 * row;
     const void* r = residual ? static_cast<const char*>(residual) + n0 * row : nullptr;
-    const bool pdl = after_route || n0 > 0;
     void* y = static_cast<char*>(Y) + n0 * row;
     rc = p->dtype == DYRA_F32
              ? moe_experts<float>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k, Wgu, Wd,
-                                  r, y, n, pdl, s)
+                                  r, y, n, s)
              : moe_experts<__nv_bfloat16>(p, x, ids + n0 * p->m.top_k, weights + n0 * p->m.top_k,
-                                          Wgu, Wd, r, y, n, pdl, s);
+                                          Wgu, Wd, r, y, n, s);
   }
   return launched(rc);
 }
@@ -246,7 +243,7 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   g.status = p->status;
   g.ws = p->ws;
   g.counters = p->tiles;
-  return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream), false));
+  return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const void* W,
@@ -288,7 +285,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
     g.J = N;
     g.K = p->d_out;
     g.Out = dX;
-    const int rc = linear(p, g, s, has_act || dbias);
+    const int rc = linear(p, g, s);
     if (rc) return launched(rc);
   }
   if (dW) {
@@ -297,7 +294,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
     g.J = p->d_out;
     g.K = N;
     g.Out = dW;
-    const int rc = linear(p, g, s, has_act || dbias || dX);
+    const int rc = linear(p, g, s);
     if (rc) return launched(rc);
   }
   return DYRA_OK;
@@ -372,7 +369,7 @@ int dyra_moe_route(dyra_moe_t p, const void* X, const void* Wr, int32_t* ids, fl
 int dyra_moe_experts(dyra_moe_t p, const void* X, const int32_t* ids, const float* weights,
                      const void* Wgu, const void* Wd, const void* residual, void* Y, int64_t N,
                      dyra_stream_t stream) {
-  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, false,
+  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -387,7 +384,7 @@ int dyra_moe_forward(dyra_moe_t p, const void* X, const void* Wr, const void* Wg
     return DYRA_ERR_ALIGNMENT;
   rc = dyra_moe_route(p, X, Wr, ids, weights, N, stream);
   if (rc) return rc;
-  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N, true,
+  return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -1,5 +1,5 @@
-// layers_f32.cu - the dense layer's fp32 products on the CUDA cores: plain FFMA
-// (TF32 tensor cores would lose ~1e-3).
+// layers_f32.cu - the fp32 products of the dense layer and of the experts on the
+// CUDA cores: plain FFMA (TF32 tensor cores would lose ~1e-3).
 //
 // An Out tile of BT x BT on 256 threads of (BT/16)^2 values each, k in steps of 32
 // through a ring of three shared-memory buffers filled by asynchronous copies.
@@ -211,6 +211,10 @@ __global__ void __launch_bounds__(256)
   using S = F32Tile<BT>;
   constexpr int V = S::V;
   extern __shared__ __align__(16) float smem[];
+  // the next grid is not let in early: its blocks, placed beside these as they
+  // leave, would share the SMs unevenly (dX and dW of 240 rows, 1346 -> 760: 79 us
+  // instead of 58)
+  sm100::pdl_wait();
   const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t tile = blockIdx.x / cs;
   const int64_t jt = tile / m_tiles;
@@ -278,6 +282,159 @@ __global__ void __launch_bounds__(256)
   cluster_sync_all();  // no CTA leaves while its part is read
 }
 
+// ---------------------------------------------------------------- experts ----
+// The experts in fp32: 64 weight rows of one expert per block against the slots
+// (token, k) that name it, sixteen at a time, k in steps of 32 through a ring of
+// four buffers. STAGE 0: rows f of the gate and of the up matrix together, hidden
+// [slot] = act(g) u; STAGE 1: rows d, part[slot]. The weights are read once for
+// every sixteen slots; four buffers of three blocks per SM keep about 100 KB of
+// them on their way. 128 threads, 4 rows (of each matrix) x 2 slots each.
+constexpr int kExRows = 64, kExSlots = 16, kExRing = 4;
+
+template <int STAGE>
+struct ExpertTile {
+  static constexpr int NG = STAGE == 0 ? 2 : 1;
+  static constexpr int Ld = kBk + 4;
+  static constexpr int Buf = (NG * kExRows + kExSlots) * Ld;
+};
+
+template <int STAGE, bool VEC>
+__global__ void __launch_bounds__(128)
+    moe_tile_kernel(MoeShape m, const float* __restrict__ In, const int* __restrict__ ids,
+                    const float* __restrict__ W, float* __restrict__ Out, int N, int* status) {
+  using S = ExpertTile<STAGE>;
+  constexpr int NG = S::NG, Ld = S::Ld, W4 = VEC ? 4 : 1;
+  extern __shared__ __align__(16) float smem[];
+  __shared__ int list[kMoeTokens * DYRA_MOE_MAX_TOP_K];
+  __shared__ int count;
+  sm100::pdl_wait();
+  const int e = blockIdx.y, tid = threadIdx.x;
+  const int slots = N * m.top_k;
+  if (tid < 32) {  // the expert's slots, in order
+    int c = 0;
+    for (int i0 = 0; i0 < slots; i0 += 32) {
+      const int i = i0 + tid;
+      const bool hit = i < slots && ids[i] == e;
+      const unsigned b = __ballot_sync(0xffffffffu, hit);
+      if (hit) list[c + __popc(b & ((1u << tid) - 1))] = i;
+      c += __popc(b);
+    }
+    if (tid == 0) count = c;
+  }
+  __syncthreads();
+  const int nsl = count;
+  if (nsl == 0) return;
+  const int rows = STAGE == 0 ? m.f : m.d, K = STAGE == 0 ? m.d : m.f;
+  const size_t wrows = STAGE == 0 ? 2 * static_cast<size_t>(m.f) : m.d;
+  const float* We = W + wrows * e * K;
+  const int r0 = blockIdx.x * kExRows;
+  const int tx = tid & 15, ty = tid >> 4;
+  const int steps = (K + kBk - 1) / kBk;
+  const uint32_t base = smem_u32(smem);
+  const size_t extent = static_cast<size_t>(slots) * rows;
+  for (int s0 = 0; s0 < nsl; s0 += kExSlots) {
+    auto issue = [&](int s) {
+      if (s < steps) {
+        const uint32_t at = base + static_cast<uint32_t>(s % kExRing) * (S::Buf * 4u);
+        const int k0 = s * kBk;
+#pragma unroll
+        for (int i = 0; i < (NG * kExRows + kExSlots) * kBk / W4 / 128; ++i) {
+          const int idx = tid + 128 * i;
+          const int k = idx % (kBk / W4) * W4, r = idx / (kBk / W4);
+          const float* row;
+          bool in = k0 + k < K;
+          if (r < NG * kExRows) {
+            const int wr = r0 + r % kExRows;
+            in = in && wr < rows;
+            row = We + static_cast<size_t>(r < kExRows ? wr : m.f + wr) * K;
+          } else {
+            const int sl = s0 + r - NG * kExRows;
+            in = in && sl < nsl;
+            const int slot = list[in ? sl : 0];
+            row = In + static_cast<size_t>(STAGE == 0 ? slot / m.top_k : slot) * K;
+          }
+          const uint32_t to = at + 4u * static_cast<uint32_t>(r * Ld + k);
+          const float* from = in ? row + k0 + k : In;
+          if (VEC)
+            sm100::cp_async_16(to, from, in ? 16u : 0u);
+          else
+            cp_async_4(to, from, in);
+        }
+      }
+      sm100::cp_async_commit();
+    };
+    f32x2 acc[NG][4][2] = {};
+#pragma unroll
+    for (int i = 0; i < kExRing - 1; ++i) issue(i);
+    for (int s = 0; s < steps; ++s) {
+      cp_async_wait<kExRing - 2>();
+      __syncthreads();
+      issue(s + kExRing - 1);
+      const float* buf = smem + static_cast<size_t>(s % kExRing) * S::Buf;
+      const float* xs = buf + NG * kExRows * Ld;
+#pragma unroll
+      for (int k = 0; k < kBk; k += 4) {
+        ulonglong2 x[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          x[j] = *reinterpret_cast<const ulonglong2*>(xs + (ty + 8 * j) * Ld + k);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(
+                buf + (g * kExRows + tx + 16 * i) * Ld + k);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              fma2(acc[g][i][j], w.x, x[j].x);
+              fma2(acc[g][i][j], w.y, x[j].y);
+            }
+          }
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // the ring starts again for the next slots
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int sl = s0 + ty + 8 * j;
+      if (sl >= nsl) continue;
+      const int slot = list[sl];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r0 + tx + 16 * i;
+        const size_t at = static_cast<size_t>(slot) * rows + row;
+        if (row >= rows || !sm100::in_bounds(status, at, 1, extent)) continue;
+        const float2 a = halves(acc[0][i][j]);
+        float v = a.x + a.y;
+        if (STAGE == 0) {
+          const float2 u = halves(acc[NG - 1][i][j]);
+          with_act(m.act, [&](auto tag) { v = act_f<decltype(tag)::value>(v) * (u.x + u.y); });
+        }
+        Out[at] = v;
+      }
+    }
+  }
+}
+
+template <int STAGE, bool VEC>
+int launch_experts(const MoeShape& m, const float* In, const int* ids, const float* W, float* Out,
+                   int N, int* status, const DeviceInfo& dev, cudaStream_t s) {
+  auto kfn = moe_tile_kernel<STAGE, VEC>;
+  static KernelSetup setup;
+  const int d = dev.device;
+  if (d < 0 || d >= kMaxDevices) return -1;
+  constexpr uint32_t smem = kExRing * ExpertTile<STAGE>::Buf * 4;
+  if (smem > setup.smem[d].load()) {
+    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return -1;
+    setup.smem[d].store(smem);
+  }
+  const int rows = STAGE == 0 ? m.f : m.d;
+  return launch_dependent(kfn, dim3((rows + kExRows - 1) / kExRows, m.experts), dim3(128), smem, 1, s,
+                          m, In, ids, W, Out, N, status);
+}
+
 template <int BT, bool AMN, bool BMN, bool VEC>
 int launch_tile(const LinearGemm& g, int cs, const DeviceInfo& dev, cudaStream_t s) {
   auto kfn = linear_f32_kernel<BT, AMN, BMN, VEC>;
@@ -293,19 +450,8 @@ int launch_tile(const LinearGemm& g, int cs, const DeviceInfo& dev, cudaStream_t
   }
   const int64_t mt = (g.M + BT - 1) / BT, jt = (g.J + BT - 1) / BT;
   if (mt * jt * cs > 0x7fffffffll) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(mt * jt * cs));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kfn, g, mt, cs) == cudaSuccess ? 0 : -1;
+  return launch_dependent(kfn, dim3(static_cast<unsigned>(mt * jt * cs)), dim3(256), smem, cs, s, g,
+                          mt, cs);
 }
 
 template <int BT>
@@ -352,6 +498,17 @@ int launch_linear_f32(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s
   if (best_bt == 128) return launch_bt<128>(g, best_cs, dev, s);
   if (best_bt == 64) return launch_bt<64>(g, best_cs, dev, s);
   return launch_bt<32>(g, best_cs, dev, s);
+}
+
+int launch_moe_tiles_f32(const MoeShape& m, const float* X, const int* ids, const float* Wgu,
+                         const float* Wd, int N, float* hidden, float* part, int* status,
+                         const DeviceInfo& dev, cudaStream_t s) {
+  const bool vec = m.d % 4 == 0 && m.f % 4 == 0;  // rows of whole 16-byte pieces
+  if (vec ? launch_experts<0, true>(m, X, ids, Wgu, hidden, N, status, dev, s)
+          : launch_experts<0, false>(m, X, ids, Wgu, hidden, N, status, dev, s))
+    return -1;
+  return vec ? launch_experts<1, true>(m, hidden, ids, Wd, part, N, status, dev, s)
+             : launch_experts<1, false>(m, hidden, ids, Wd, part, N, status, dev, s);
 }
 
 }  // namespace dyra

@@ -378,8 +378,7 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
                             const float* weights, const __nv_bfloat16* Wgu,
                             const __nv_bfloat16* Wd, const __nv_bfloat16* residual,
                             __nv_bfloat16* Y, int N, __nv_bfloat16* hidden, float* ws,
-                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s,
-                            bool pdl) {
+                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s) {
   const int nb = ceil_div(N, 16) * 16;
   const int reached = std::min(m.experts, N * m.top_k);
   const MoeTables t{ids, weights, N, m.top_k, m.experts};
@@ -405,21 +404,11 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
   const uint32_t smem_d = stream_setup<DownPolicy>(w.c, nb, false, false, ws, nullptr, status, dev);
   if (!smem_g || !smem_d) return -3;
   w.c.late_b = 1;
-  if (stream_launch<GateUpPolicy>(g, smem_g, dev, s, pdl)) return -1;
-  if (stream_launch<DownPolicy>(w, smem_d, dev, s, true)) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(static_cast<int64_t>(m.d) / 8 * N, 128)));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_join_kernel, w.c, static_cast<const int*>(w.meta), residual,
-                            Y, N, m.d) == cudaSuccess
-             ? 0
-             : -1;
+  if (stream_launch<GateUpPolicy>(g, smem_g, dev, s)) return -1;
+  if (stream_launch<DownPolicy>(w, smem_d, dev, s)) return -1;
+  const dim3 grid(static_cast<unsigned>(ceil_div(static_cast<int64_t>(m.d) / 8 * N, 128)));
+  return launch_dependent(moe_join_kernel, grid, dim3(128), 0, 1, s, w.c,
+                          static_cast<const int*>(w.meta), residual, Y, N, m.d);
 }
 
 }  // namespace dyra

@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearGemm g, int64_t 
   __shared__ float Bs[kSimtBk][kSimtBt + 1];
   const T* __restrict__ A = static_cast<const T*>(g.A);
   const T* __restrict__ B = static_cast<const T*>(g.B);
+  sm100::pdl_launch_dependents();
+  sm100::pdl_wait();
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t jt = blockIdx.x / m_tiles;
   const int64_t m0 = (blockIdx.x - jt * m_tiles) * kSimtBt, j0 = jt * kSimtBt;
@@ -80,6 +82,8 @@ __global__ void __launch_bounds__(256)
   struct alignas(sizeof(T) * V) P {
     T v[V];
   };
+  if (sizeof(T) == 2) sm100::pdl_launch_dependents();  // not before the fp32 products: layers_f32.cu
+  sm100::pdl_wait();
   const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int col = (blockIdx.x * 32 + lane) * V;
   float sum[V] = {};
@@ -158,11 +162,12 @@ int launch_act_backward_v(const T* dY, const T* Z, int act, T* dZ, T* dbias, int
   const int64_t want = std::max<int64_t>(1, 4 * dev.sm_count / cols);
   const int chunks = static_cast<int>(
       std::min<int64_t>({want, std::max<int64_t>(1, (N + 7) / 8), kColSumChunks}));
+  int rc = -1;
   with_act_host(act, [&](auto tag) {
-    act_backward_kernel<T, V, decltype(tag)::value><<<dim3(cols, chunks), 256, 0, s>>>(
-        dY, Z, dZ, dbias, N, d_out, partial, counters, status);
+    rc = launch_dependent(act_backward_kernel<T, V, decltype(tag)::value>, dim3(cols, chunks),
+                          dim3(256), 0, 1, s, dY, Z, dZ, dbias, N, d_out, partial, counters, status);
   });
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return rc;
 }
 
 // ----------------------------------------------------------------- router ----
@@ -206,6 +211,7 @@ __global__ void __launch_bounds__(256)
   __shared__ double pick[R][DYRA_MOE_MAX_EXPERTS];
   __shared__ int last;
   sm100::pdl_launch_dependents();  // the experts' kernel may set up meanwhile
+  sm100::pdl_wait();
   const int e0 = blockIdx.x * R, n0 = blockIdx.y * R;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double acc[R][R] = {};
@@ -306,11 +312,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- experts ----
-// CUDA-core experts: a warp per output row of one expert, over the slots
-// (token, k) that name it, up to eight at a time: each weight is read once per
-// eight slots. STAGE 0: hidden[slot] = act(g) u over rows f; STAGE 1: part[slot]
-// over rows d. The slots of the block's expert are listed in order first. VEC: the
-// rows are whole 16-byte pieces.
+// CUDA-core experts (fp32 with few slots per expert, and bf16 for debugging): a warp
+// per output row of one expert, over the slots (token, k) that name it, up to eight at
+// a time: each weight is read once per eight slots. STAGE 0: hidden[slot] = act(g) u
+// over rows f; STAGE 1: part[slot] over rows d. The slots of the block's expert are
+// listed in order first. VEC: the rows are whole 16-byte pieces.
 template <typename T, int STAGE, bool VEC, int NS>
 __device__ __forceinline__ void expert_row(const MoeShape& m, const T* __restrict__ In,
                                            const T* __restrict__ w0, const T* __restrict__ w1,
@@ -431,14 +437,10 @@ __global__ void __launch_bounds__(256)
 int launch_linear_simt(const LinearGemm& g, const DeviceInfo&, cudaStream_t s) {
   const int64_t mt = (g.M + kSimtBt - 1) / kSimtBt, jt = (g.J + kSimtBt - 1) / kSimtBt;
   if (mt * jt > 0x7fffffffll) return -1;
-  const dim3 grid(static_cast<unsigned>(mt * jt));
-  if (g.a_mn && g.b_mn)
-    linear_simt_kernel<true, true><<<grid, 256, 0, s>>>(g, mt);
-  else if (g.a_mn)
-    linear_simt_kernel<true, false><<<grid, 256, 0, s>>>(g, mt);
-  else
-    linear_simt_kernel<false, false><<<grid, 256, 0, s>>>(g, mt);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  auto kfn = g.a_mn && g.b_mn ? linear_simt_kernel<true, true>
+             : g.a_mn         ? linear_simt_kernel<true, false>
+                              : linear_simt_kernel<false, false>;
+  return launch_dependent(kfn, dim3(static_cast<unsigned>(mt * jt)), dim3(256), 0, 1, s, g, mt);
 }
 
 int col_sum_blocks(int d_out) { return (d_out + 31) / 32; }
@@ -474,10 +476,11 @@ int launch_moe_route(const MoeShape& m, const T* X, const T* Wr, int* ids, float
     const int n = static_cast<int>(std::min<int64_t>(kRouteTokens, N - n0));
     const dim3 grid((m.experts + kRouteTile - 1) / kRouteTile, (n + kRouteTile - 1) / kRouteTile);
     auto kfn = vec ? moe_route_kernel<T, true> : moe_route_kernel<T, false>;
-    kfn<<<grid, 256, 0, s>>>(m, X + n0 * m.d, Wr, ids + n0 * m.top_k, weights + n0 * m.top_k,
-                             logits, counters, n);
+    if (launch_dependent(kfn, grid, dim3(256), 0, 1, s, m, X + n0 * m.d, Wr, ids + n0 * m.top_k,
+                         weights + n0 * m.top_k, logits, counters, n))
+      return -1;
   }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return 0;
 }
 template int launch_moe_route<float>(const MoeShape&, const float*, const float*, int*, float*,
                                      int64_t, double*, int*, cudaStream_t);
@@ -488,41 +491,36 @@ template int launch_moe_route<__nv_bfloat16>(const MoeShape&, const __nv_bfloat1
 template <typename T>
 int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const float* weights,
                             const T* Wgu, const T* Wd, const T* residual, T* Y, int N, T* hidden,
-                            float* part, int* status, cudaStream_t s, bool pdl) {
-  const bool vec = m.d * sizeof(T) % 16 == 0 && m.f * sizeof(T) % 16 == 0;
-  auto up = vec ? moe_expert_kernel<T, 0, true> : moe_expert_kernel<T, 0, false>;
-  auto down = vec ? moe_expert_kernel<T, 1, true> : moe_expert_kernel<T, 1, false>;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.gridDim = dim3((m.f + 7) / 8, m.experts);
-  cfg.numAttrs = pdl ? 1 : 0;
-  if (cudaLaunchKernelEx(&cfg, up, m, X, ids, Wgu, hidden, static_cast<float*>(nullptr), N,
-                         status) != cudaSuccess)
-    return -1;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3((m.d + 7) / 8, m.experts);
-  if (cudaLaunchKernelEx(&cfg, down, m, static_cast<const T*>(hidden), ids, Wd,
-                         static_cast<T*>(nullptr), part, N, status) != cudaSuccess)
-    return -1;
-  cfg.gridDim = dim3((m.d + 255) / 256, N);
-  return cudaLaunchKernelEx(&cfg, moe_combine_kernel<T>, m, ids, weights,
-                            static_cast<const float*>(part), residual, Y, N,
-                            status) == cudaSuccess
-             ? 0
-             : -1;
+                            float* part, int* status, const DeviceInfo& dev, cudaStream_t s) {
+  bool tiles = false;
+  if constexpr (sizeof(T) == 4) {
+    // tiles of sixteen slots where the experts have about as many each: 280 slots on
+    // 19 experts of 247 x 4961 take 392 us in tiles, 742 by rows, 60 slots on 7 of 603
+    // x 180 45 and 32 (a tile's long sums are one block's)
+    tiles = N * m.top_k >= 12 * m.experts;
+    if (tiles && launch_moe_tiles_f32(m, X, ids, Wgu, Wd, N, hidden, part, status, dev, s)) return -1;
+  }
+  if (!tiles) {
+    const bool vec = m.d * sizeof(T) % 16 == 0 && m.f * sizeof(T) % 16 == 0;
+    auto up = vec ? moe_expert_kernel<T, 0, true> : moe_expert_kernel<T, 0, false>;
+    auto down = vec ? moe_expert_kernel<T, 1, true> : moe_expert_kernel<T, 1, false>;
+    if (launch_dependent(up, dim3((m.f + 7) / 8, m.experts), dim3(256), 0, 1, s, m, X, ids, Wgu,
+                         hidden, static_cast<float*>(nullptr), N, status) ||
+        launch_dependent(down, dim3((m.d + 7) / 8, m.experts), dim3(256), 0, 1, s, m,
+                         static_cast<const T*>(hidden), ids, Wd, static_cast<T*>(nullptr), part, N,
+                         status))
+      return -1;
+  }
+  return launch_dependent(moe_combine_kernel<T>, dim3((m.d + 255) / 256, N), dim3(256), 0, 1, s, m,
+                          ids, weights, static_cast<const float*>(part), residual, Y, N, status);
 }
 template int launch_moe_experts_simt<float>(const MoeShape&, const float*, const int*,
                                             const float*, const float*, const float*, const float*,
-                                            float*, int, float*, float*, int*, cudaStream_t,
-                                            bool);
+                                            float*, int, float*, float*, int*, const DeviceInfo&,
+                                            cudaStream_t);
 template int launch_moe_experts_simt<__nv_bfloat16>(
     const MoeShape&, const __nv_bfloat16*, const int*, const float*, const __nv_bfloat16*,
     const __nv_bfloat16*, const __nv_bfloat16*, __nv_bfloat16*, int, __nv_bfloat16*, float*, int*,
-    cudaStream_t, bool);
+    const DeviceInfo&, cudaStream_t);
 
 }  // namespace dyra

@@ -366,8 +366,7 @@ PairPlan plan_pairs(const LinearGemm& g, const DeviceInfo& dev) {
 }
 
 template <bool kRowMn, bool kColMn, PairEpilogue kMode, bool kTail>
-int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaStream_t s,
-                   bool pdl) {
+int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaStream_t s) {
   using Pol = DensePairPolicy<kRowMn, kColMn, kMode, kTail>;
   DensePairParams p;
   p.J = static_cast<int>(g.J);
@@ -399,14 +398,14 @@ int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaSt
                         kColMn, g.status, dev);
   if (!smem) return -3;
   p.c.idesc = idesc_bf16(256, p.bn, kRowMn, kColMn);
-  return launch_gemm_pair<Pol>(p, smem, dev, s, pdl);
+  return launch_gemm_pair<Pol>(p, smem, dev, s, true);
 }
 
 template <bool kRowMn, bool kColMn, PairEpilogue kMode>
-int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+int launch_pair(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s) {
   const int split = plan_pairs(g, dev).split;
-  return split > 1 ? launch_pair_as<kRowMn, kColMn, kMode, true>(g, split, dev, s, pdl)
-                   : launch_pair_as<kRowMn, kColMn, kMode, false>(g, 1, dev, s, pdl);
+  return split > 1 ? launch_pair_as<kRowMn, kColMn, kMode, true>(g, split, dev, s)
+                   : launch_pair_as<kRowMn, kColMn, kMode, false>(g, 1, dev, s);
 }
 
 // --------------------------------------------------------------- clusters ----
@@ -497,8 +496,7 @@ struct SplitChoice {
 };
 
 template <bool kAMn, bool kBMn, bool kEpi>
-int launch_split(const LinearGemm& g, SplitChoice ch, const DeviceInfo& dev, cudaStream_t s,
-                 bool pdl) {
+int launch_split(const LinearGemm& g, SplitChoice ch, const DeviceInfo& dev, cudaStream_t s) {
   using Pol = DenseSplitPolicy<kAMn, kBMn, kEpi>;
   DenseSplitParams p;
   p.M = static_cast<int>(g.M);
@@ -517,7 +515,7 @@ int launch_split(const LinearGemm& g, SplitChoice ch, const DeviceInfo& dev, cud
   const uint32_t smem =
       stream_setup<Pol>(p.c, ch.nb, kAMn, kBMn, nullptr, nullptr, g.status, dev);
   if (!smem) return -3;
-  return split_launch<Pol>(p, ceil_div(g.M, 128) * p.tiles_j, ch.cs, smem, dev, s, pdl);
+  return split_launch<Pol>(p, ceil_div(g.M, 128) * p.tiles_j, ch.cs, smem, dev, s);
 }
 
 // Clusters of cs CTAs (one CTA per SM) that run at once: a cluster stays within
@@ -575,19 +573,19 @@ size_t linear_ws_bytes(const DeviceInfo& dev) {  // a part of 256 x 256 per pair
 }
 int linear_counters(const DeviceInfo& dev) { return dev.sm_count; }
 
-int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+int launch_linear_umma(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s) {
   const SplitChoice ch = choose_split(g, dev);
 
   if (g.a_mn && g.b_mn)
-    return ch.nb ? launch_split<true, true, false>(g, ch, dev, s, pdl)
-                 : launch_pair<true, true, kPlain>(g, dev, s, pdl);
+    return ch.nb ? launch_split<true, true, false>(g, ch, dev, s)
+                 : launch_pair<true, true, kPlain>(g, dev, s);
   if (g.a_mn)
-    return ch.nb ? launch_split<true, false, false>(g, ch, dev, s, pdl)
-                 : launch_pair<false, true, kPlain>(g, dev, s, pdl);
-  if (ch.nb) return launch_split<false, false, true>(g, ch, dev, s, pdl);
-  if (g.Z) return launch_pair<false, false, kForwardZ>(g, dev, s, pdl);
-  return g.residual ? launch_pair<false, false, kForwardResidual>(g, dev, s, pdl)
-                    : launch_pair<false, false, kForward>(g, dev, s, pdl);
+    return ch.nb ? launch_split<true, false, false>(g, ch, dev, s)
+                 : launch_pair<false, true, kPlain>(g, dev, s);
+  if (ch.nb) return launch_split<false, false, true>(g, ch, dev, s);
+  if (g.Z) return launch_pair<false, false, kForwardZ>(g, dev, s);
+  return g.residual ? launch_pair<false, false, kForwardResidual>(g, dev, s)
+                    : launch_pair<false, false, kForward>(g, dev, s);
 }
 
 }  // namespace dyra

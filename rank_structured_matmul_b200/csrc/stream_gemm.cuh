@@ -31,6 +31,7 @@
 //   static void nothing(p, epi);            // there are no steps at all
 #pragma once
 
+#include "layers.h"
 #include "umma_common.cuh"
 
 namespace dyra {
@@ -549,21 +550,12 @@ int raise_smem(Kernel kfn, KernelSetup& setup, uint32_t smem, const DeviceInfo& 
 
 template <class Pol>
 int stream_launch(const typename Pol::Params& p, uint32_t smem, const DeviceInfo& dev,
-                  cudaStream_t s, bool pdl) {
+                  cudaStream_t s) {
   auto kfn = stream_kernel<Pol>;
   static KernelSetup setup;
   if (raise_smem(kfn, setup, smem, dev)) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count));
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kfn, p) == cudaSuccess ? 0 : -1;
+  return launch_dependent(kfn, dim3(static_cast<unsigned>(dev.sm_count)), dim3(kStreamThreads),
+                          smem, 1, s, p);
 }
 
 // Clusters of cs CTAs that can be resident at once, at a CTA per SM.
@@ -593,30 +585,12 @@ int split_resident(int cs, const DeviceInfo& dev) {
 
 template <class Pol>
 int split_launch(const typename Pol::Params& p, int tiles, int cs, uint32_t smem,
-                 const DeviceInfo& dev, cudaStream_t s, bool pdl) {
+                 const DeviceInfo& dev, cudaStream_t s) {
   auto kfn = split_kernel<Pol>;
   static KernelSetup setup;
   if (raise_smem(kfn, setup, smem, dev)) return -1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * cs));
-  cfg.blockDim = dim3(kStreamThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int na = 0;
-  if (pdl) {
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cs > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = static_cast<unsigned>(cs);
-    attr[na].val.clusterDim.y = 1;
-    attr[na++].val.clusterDim.z = 1;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = static_cast<unsigned>(na);
-  return cudaLaunchKernelEx(&cfg, kfn, p, cs) == cudaSuccess ? 0 : -1;
+  return launch_dependent(kfn, dim3(static_cast<unsigned>(tiles * cs)), dim3(kStreamThreads), smem,
+                          cs, s, p, cs);
 }
 
 }  // namespace dyra

@@ -490,7 +490,7 @@ MOE_BF16 = [(1, 64, 64, 4, 1), (1, 512, 1024, 8, 2), (2, 128, 72, 8, 8), (3, 100
             (7, 136, 200, 64, 4), (16, 256, 512, 8, 2), (17, 264, 136, 5, 2), (33, 2048, 128, 9, 3),
             (64, 512, 256, 128, 8), (64, 8, 8, 3, 3), (1, 4096, 2048, 2, 2), (48, 72, 1032, 300, 16),
             (33, 16, 24, 512, 16), (5, 1288, 8, 3, 1), (40, 8, 2056, 2, 2)]
-MOE_F32 = [(1, 1, 1, 1, 1), (3, 256, 512, 8, 2), (5, 33, 17, 6, 3), (64, 65, 70, 12, 4),
+MOE_F32 = [(1, 1, 1, 1, 1), (50, 136, 200, 3, 2), (61, 33, 70, 2, 2), (64, 5, 129, 1, 1), (3, 256, 512, 8, 2), (5, 33, 17, 6, 3), (64, 65, 70, 12, 4),
            (2, 1000, 251, 4, 2)]
 
 
@@ -700,6 +700,45 @@ def test_moe_refusals_on_the_device():
     torch.cuda.synchronize()
     assert bool((Y == 7.0).all()) and layer.status() == 0
     layer.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 16, 300])
+def test_calls_in_a_row(N, dtype):
+    """A block's calls in a row, each reading what the one before wrote, over and
+    over the same buffers: every kernel is set up while the one before it runs, so
+    the chain's bits must be those of the same calls with a wait after each."""
+    d, f, E, K = 256, 520, 9, 2
+    fc1, fc2 = layers.DenseLinear(d, f, dtype), layers.DenseLinear(f, d, dtype)
+    moe = layers.MoeLayer(d, 136, E, K, dtype)
+    X, W1, b1, _ = dense_case(N, d, f, dtype, seed=1)
+    _, W2, b2, _ = dense_case(N, f, d, dtype, seed=2)
+    _, Wr, Wgu, Wd, _ = moe_case(N, d, 136, E, K, dtype)
+
+    def chain(wait):
+        x, out = X.clone(), []
+        for _ in range(8):
+            h, Z = fc1.forward(x, W1, bias=b1, act="gelu", save_z=True)
+            wait()
+            fc2.forward(h, W2, bias=b2, residual=x, Y=x)
+            wait()
+            y, ids, w = moe.forward(x, Wr, Wgu, Wd)
+            wait()
+            dx, dw, db = fc1.backward(h, y, W1, Z=Z, act="gelu")
+            wait()
+            torch.add(y, dx, alpha=0.01, out=x)
+            wait()
+            x.div_(x.float().std().to(x.dtype))
+            wait()
+            out += [ids, w, dw, db, x.clone()]
+        return out
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, c in zip(chain(lambda: None), want):
+            assert torch.equal(a, c)
+    assert fc1.status() == 0 and fc2.status() == 0 and moe.status() == 0
+    fc1.close(), fc2.close(), moe.close()
 
 
 @pytest.mark.parametrize("N", [1, 100])
