@@ -287,8 +287,8 @@ __global__ void __launch_bounds__(256)
 // (token, k) that name it, sixteen at a time, k in steps of 32 through a ring of
 // four buffers. STAGE 0: rows f of the gate and of the up matrix together, hidden
 // [slot] = act(g) u; STAGE 1: rows d, part[slot]. The weights are read once for
-// every sixteen slots; four buffers of three blocks per SM keep about 100 KB of
-// them on their way. 128 threads, 4 rows (of each matrix) x 2 slots each.
+// every sixteen slots; 128 threads, 4 rows (of each matrix) x 2 slots each. A cluster
+// of cs blocks shares the steps of a tile, as in the dense products.
 constexpr int kExRows = 64, kExSlots = 16, kExRing = 4;
 
 template <int STAGE>
@@ -301,7 +301,7 @@ struct ExpertTile {
 template <int STAGE, bool VEC>
 __global__ void __launch_bounds__(128)
     moe_tile_kernel(MoeShape m, const float* __restrict__ In, const int* __restrict__ ids,
-                    const float* __restrict__ W, float* __restrict__ Out, int N, int* status) {
+                    const float* __restrict__ W, float* __restrict__ Out, int N, int* status, int cs) {
   using S = ExpertTile<STAGE>;
   constexpr int NG = S::NG, Ld = S::Ld, W4 = VEC ? 4 : 1;
   extern __shared__ __align__(16) float smem[];
@@ -327,16 +327,18 @@ __global__ void __launch_bounds__(128)
   const int rows = STAGE == 0 ? m.f : m.d, K = STAGE == 0 ? m.d : m.f;
   const size_t wrows = STAGE == 0 ? 2 * static_cast<size_t>(m.f) : m.d;
   const float* We = W + wrows * e * K;
-  const int r0 = blockIdx.x * kExRows;
+  const int rank = cs > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int r0 = static_cast<int>(blockIdx.x) / cs * kExRows;
   const int tx = tid & 15, ty = tid >> 4;
-  const int steps = (K + kBk - 1) / kBk;
+  const int all = (K + kBk - 1) / kBk;
+  const int first = rank * all / cs, steps = (rank + 1) * all / cs - first;
   const uint32_t base = smem_u32(smem);
   const size_t extent = static_cast<size_t>(slots) * rows;
   for (int s0 = 0; s0 < nsl; s0 += kExSlots) {
     auto issue = [&](int s) {
       if (s < steps) {
         const uint32_t at = base + static_cast<uint32_t>(s % kExRing) * (S::Buf * 4u);
-        const int k0 = s * kBk;
+        const int k0 = (first + s) * kBk;
 #pragma unroll
         for (int i = 0; i < (NG * kExRows + kExSlots) * kBk / W4 / 128; ++i) {
           const int idx = tid + 128 * i;
@@ -393,26 +395,50 @@ __global__ void __launch_bounds__(128)
       }
     }
     cp_async_wait<0>();
-    __syncthreads();  // the ring starts again for the next slots
+    __syncthreads();  // the ring is free
+    auto out = [&](int sl, int r, float v, float u) {
+      const int row = r0 + r;
+      if (sl >= nsl || row >= rows) return;
+      const size_t at = static_cast<size_t>(list[sl]) * rows + row;
+      if (!sm100::in_bounds(status, at, 1, extent)) return;
+      if (STAGE == 0)
+        with_act(m.act, [&](auto tag) { v = act_f<decltype(tag)::value>(v) * u; });
+      Out[at] = v;
+    };
+    if (cs == 1) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int sl = s0 + ty + 8 * j;
-      if (sl >= nsl) continue;
-      const int slot = list[sl];
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = r0 + tx + 16 * i;
-        const size_t at = static_cast<size_t>(slot) * rows + row;
-        if (row >= rows || !sm100::in_bounds(status, at, 1, extent)) continue;
-        const float2 a = halves(acc[0][i][j]);
-        float v = a.x + a.y;
-        if (STAGE == 0) {
-          const float2 u = halves(acc[NG - 1][i][j]);
-          with_act(m.act, [&](auto tag) { v = act_f<decltype(tag)::value>(v) * (u.x + u.y); });
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = halves(acc[0][i][j]), u = halves(acc[NG - 1][i][j]);
+          out(s0 + ty + 8 * j, tx + 16 * i, a.x + a.y, u.x + u.y);
         }
-        Out[at] = v;
-      }
+      continue;
     }
+    // the part [slot][matrix][row], then a share of the values summed over the parts
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = halves(acc[g][i][j]);
+          smem[((ty + 8 * j) * NG + g) * kExRows + tx + 16 * i] = a.x + a.y;
+        }
+    cluster_sync_all();
+    constexpr int Values = kExSlots * kExRows;
+    for (int i = rank * Values / cs + tid; i < (rank + 1) * Values / cs; i += 128) {
+      const int sl = i / kExRows, r = i % kExRows;
+      float v = 0.f, u = 0.f;
+      for (int q = 0; q < cs; ++q) {
+        const uint32_t at = mapa_shared(base + 4u * static_cast<uint32_t>(sl * NG * kExRows + r),
+                                        static_cast<uint32_t>(q));
+        v += ld_shared_cluster(at);
+        if (STAGE == 0) u += ld_shared_cluster(at + 4u * kExRows);
+      }
+      out(s0 + sl, r, v, u);
+    }
+    cluster_sync_all();  // the parts have been read: the ring may start again
   }
 }
 
@@ -430,9 +456,13 @@ int launch_experts(const MoeShape& m, const float* In, const int* ids, const flo
       return -1;
     setup.smem[d].store(smem);
   }
-  const int rows = STAGE == 0 ? m.f : m.d;
-  return launch_dependent(kfn, dim3((rows + kExRows - 1) / kExRows, m.experts), dim3(128), smem, 1, s,
-                          m, In, ids, W, Out, N, status);
+  const int rows = STAGE == 0 ? m.f : m.d, steps = ((STAGE == 0 ? m.d : m.f) + kBk - 1) / kBk;
+  const int tiles = (rows + kExRows - 1) / kExRows, reached = std::min(m.experts, N * m.top_k);
+  // clusters while the blocks are fewer than two per SM and each keeps four steps
+  int cs = 1;
+  while (cs < 8 && tiles * reached * cs < 2 * dev.sm_count && 8 * cs <= steps) cs *= 2;
+  return launch_dependent(kfn, dim3(tiles * cs, m.experts), dim3(128), smem, cs, s, m, In, ids, W,
+                          Out, N, status, cs);
 }
 
 template <int BT, bool AMN, bool BMN, bool VEC>

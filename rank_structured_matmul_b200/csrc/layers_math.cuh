@@ -118,7 +118,7 @@ __device__ __forceinline__ float act_grad_f(float z) {
 template <typename T>
 constexpr bool kFastMath = sizeof(T) == 2;
 
-// Calls f with a tag for the run-time activation, so that loops over values
+// A constant as an argument. with_act calls f with a tag for the run-time activation, so that loops over values
 // hold one activation's code.
 template <int V>
 struct ActTag {

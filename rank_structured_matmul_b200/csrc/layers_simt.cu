@@ -316,53 +316,75 @@ __global__ void __launch_bounds__(256)
 // per output row of one expert, over the slots (token, k) that name it, up to eight at
 // a time: each weight is read once per eight slots. STAGE 0: hidden[slot] = act(g) u
 // over rows f; STAGE 1: part[slot] over rows d. The slots of the block's expert are
-// listed in order first. VEC: the rows are whole 16-byte pieces.
+// listed in order first. VEC: the rows are whole 16-byte pieces. A warp's time is the
+// latency of its loads; two rows per warp, for half the loads of x, were slower (151
+// against 94 us for 14 tokens on 5 experts of 601 x 1935).
+
+// The sums over the warp of n values each lane holds: at each step a lane keeps half
+// of its values and hands the other half to its partner, so lane l ends with value
+// l / (32 / n) (n a power of two, at most 32).
+template <int n>
+__device__ __forceinline__ float sums_to_lanes(float (&v)[n], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int h = n / 2; h > 0; h >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = upper ? v[i] : v[i + h], keep = upper ? v[i + h] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+#pragma unroll
+  for (int q = 32 / n / 2; q > 0; q >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], q);
+  return v[0];
+}
+
 template <typename T, int STAGE, bool VEC, int NS>
 __device__ __forceinline__ void expert_row(const MoeShape& m, const T* __restrict__ In,
-                                           const T* __restrict__ w0, const T* __restrict__ w1,
-                                           const int* list, int K, int rows, int row, int lane,
-                                           T* __restrict__ hidden, float* __restrict__ part,
-                                           size_t extent, int* status) {
-  constexpr int W = VEC ? 16 / sizeof(T) : 1;
+                                            const T* __restrict__ We, const int* list, int K,
+                                            int rows, int row, int lane, T* __restrict__ hidden,
+                                            float* __restrict__ part, size_t extent, int* status) {
+  constexpr int W = VEC ? 16 / sizeof(T) : 1, NG = STAGE == 0 ? 2 : 1;
   struct alignas(W * sizeof(T)) P {
     T v[W];
   };
   const T* x[NS];
-  float a0[NS] = {}, a1[NS] = {};
+  const T* w[NG];
+  float a[NG * NS] = {};
 #pragma unroll
   for (int q = 0; q < NS; ++q)
     x[q] = In + static_cast<size_t>(STAGE == 0 ? list[q] / m.top_k : list[q]) * K;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) w[g] = We + static_cast<size_t>(g * m.f + row) * K;
 #pragma unroll 4
   for (int i = lane * W; i < K; i += 32 * W) {
-    const P p0 = *reinterpret_cast<const P*>(w0 + i);
-    P p1 = p0;
-    if (STAGE == 0) p1 = *reinterpret_cast<const P*>(w1 + i);
+    P pw[NG], px[NS];
 #pragma unroll
-    for (int q = 0; q < NS; ++q) {
-      const P px = *reinterpret_cast<const P*>(x[q] + i);
+    for (int g = 0; g < NG; ++g) pw[g] = *reinterpret_cast<const P*>(w[g] + i);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        a0[q] = fmaf(load_f(p0.v[j]), load_f(px.v[j]), a0[q]);
-        if (STAGE == 0) a1[q] = fmaf(load_f(p1.v[j]), load_f(px.v[j]), a1[q]);
-      }
-    }
+    for (int q = 0; q < NS; ++q) px[q] = *reinterpret_cast<const P*>(x[q] + i);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int q = 0; q < NS; ++q)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          a[g * NS + q] = fmaf(load_f(pw[g].v[j]), load_f(px[q].v[j]), a[g * NS + q]);
   }
-#pragma unroll
-  for (int q = 0; q < NS; ++q) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a0[q] += __shfl_xor_sync(0xffffffffu, a0[q], o);
-      if (STAGE == 0) a1[q] += __shfl_xor_sync(0xffffffffu, a1[q], o);
-    }
-    const size_t at = static_cast<size_t>(list[q]) * rows + row;
-    if (lane != 0 || !sm100::in_bounds(status, at, 1, extent)) continue;
-    if (STAGE == 0)
-      with_act(m.act, [&](auto tag) {
-        hidden[at] = store_f<T>(act_f<decltype(tag)::value, kFastMath<T>>(a0[q]) * a1[q]);
-      });
-    else
-      part[at] = a0[q];
-  }
+  constexpr int n = NG * NS, share = 32 / n;  // lanes per value
+  const float v = sums_to_lanes<n>(a, lane);
+  const float up = STAGE == 0 ? __shfl_xor_sync(0xffffffffu, v, 16) : 0.f;
+  const int q = lane / share;
+  if (lane % share != 0 || q >= NS) return;
+  const size_t at = static_cast<size_t>(list[q]) * rows + row;
+  if (!sm100::in_bounds(status, at, 1, extent)) return;
+  if (STAGE == 0)
+    with_act(m.act, [&](auto tag) {
+      hidden[at] = store_f<T>(act_f<decltype(tag)::value, kFastMath<T>>(v) * up);
+    });
+  else
+    part[at] = v;
 }
 
 template <typename T, int STAGE, bool VEC>
@@ -396,18 +418,17 @@ __global__ void __launch_bounds__(256)
   const size_t extent = static_cast<size_t>(slots) * rows;
   const int row = blockIdx.x * 8 + warp;
   if (row >= rows) return;
-  const T* w0 = We + static_cast<size_t>(row) * K;
-  const T* w1 = STAGE == 0 ? We + static_cast<size_t>(m.f + row) * K : w0;
   int s0 = 0;
-  for (; s0 + 8 <= nsl; s0 += 8)
-    expert_row<T, STAGE, VEC, 8>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
-                                 status);
-  for (; s0 + 3 <= nsl; s0 += 3)
-    expert_row<T, STAGE, VEC, 3>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
-                                 status);
-  for (; s0 < nsl; ++s0)
-    expert_row<T, STAGE, VEC, 1>(m, In, w0, w1, list + s0, K, rows, row, lane, hidden, part, extent,
-                                 status);
+  auto take = [&](auto tag) {
+    constexpr int NS = decltype(tag)::value;
+    for (; s0 + NS <= nsl; s0 += NS)
+      expert_row<T, STAGE, VEC, NS>(m, In, We, list + s0, K, rows, row, lane, hidden, part, extent,
+                                    status);
+  };
+  take(ActTag<8>());
+  take(ActTag<4>());
+  take(ActTag<2>());
+  take(ActTag<1>());
 }
 
 // Y[n] = sum over k, in order, of weights[n][k] part[n][k] + residual[n]
@@ -495,8 +516,8 @@ int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const
   bool tiles = false;
   if constexpr (sizeof(T) == 4) {
     // tiles of sixteen slots where the experts have about as many each: 280 slots on
-    // 19 experts of 247 x 4961 take 392 us in tiles, 742 by rows, 60 slots on 7 of 603
-    // x 180 45 and 32 (a tile's long sums are one block's)
+    // 19 experts of 247 x 4961 take 278 us in tiles and took 742 by rows, 60 slots on 7
+    // of 603 x 180 take 32 and 26
     tiles = N * m.top_k >= 12 * m.experts;
     if (tiles && launch_moe_tiles_f32(m, X, ids, Wgu, Wd, N, hidden, part, status, dev, s)) return -1;
   }
