@@ -92,20 +92,7 @@ __device__ __forceinline__ int side_row(int t, int v) {
 // Two fp32 FMAs in one instruction on the halves of 64-bit registers, which halves
 // the issue slots of the inner product (dW of 512 rows, 2048 -> 2048: 150 -> 109 us
 // with 128 tiles; the forward, bound by its shared-memory loads, is as before).
-typedef unsigned long long f32x2;
-__device__ __forceinline__ void fma2(f32x2& d, f32x2 a, f32x2 b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ f32x2 twice(float v) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float2 halves(f32x2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
+__device__ __forceinline__ void add_product(f32x2& d, f32x2 a, f32x2 b) { d = fma2(a, b, d); }
 
 // A's side of the product, four k of a buffer: acc(y, x) += sum over k of a b.
 // K-major A (then B is K-major too): the halves are even and odd k, both operands
@@ -133,11 +120,11 @@ struct Product {
 #pragma unroll
       for (int y = 0; y < V; ++y)
 #pragma unroll
-        for (int x = 0; x < V; ++x) fma2(acc[y][x], a[x].x, b[y].x);
+        for (int x = 0; x < V; ++x) add_product(acc[y][x], a[x].x, b[y].x);
 #pragma unroll
       for (int y = 0; y < V; ++y)
 #pragma unroll
-        for (int x = 0; x < V; ++x) fma2(acc[y][x], a[x].y, b[y].y);
+        for (int x = 0; x < V; ++x) add_product(acc[y][x], a[x].y, b[y].y);
     } else {
       float b[4][V];
       if constexpr (!BMN) {
@@ -176,9 +163,9 @@ struct Product {
         }
 #pragma unroll
         for (int y = 0; y < V; ++y) {
-          const f32x2 by = twice(b[q][y]);
+          const f32x2 by = pair(b[q][y], b[q][y]);
 #pragma unroll
-          for (int x = 0; x < XN; ++x) fma2(acc[y][x], a[x], by);
+          for (int x = 0; x < XN; ++x) add_product(acc[y][x], a[x], by);
         }
       }
     }
@@ -388,8 +375,8 @@ __global__ void __launch_bounds__(128)
                 buf + (g * kExRows + tx + 16 * i) * Ld + k);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              fma2(acc[g][i][j], w.x, x[j].x);
-              fma2(acc[g][i][j], w.y, x[j].y);
+              add_product(acc[g][i][j], w.x, x[j].x);
+              add_product(acc[g][i][j], w.y, x[j].y);
             }
           }
       }

@@ -114,6 +114,58 @@ __device__ __forceinline__ float act_grad_f(float z) {
   return 1.f;
 }
 
+// Two fp32 operations in one instruction, on the halves of 64-bit registers.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// act_f<ACT, true> of eight values; the GELU's polynomial two values at a time,
+// which nearly halves its instructions.
+template <int ACT>
+__device__ __forceinline__ void act8(float (&v)[8]) {
+  if constexpr (ACT == DYRA_ACT_GELU) {
+    constexpr float C[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
+                            -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
+                            2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float x0 = fminf(fabsf(v[i]), 12.f), x1 = fminf(fabsf(v[i + 1]), 12.f);
+      const f32x2 x = pair(x0, x1);
+      const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
+      f32x2 q = pair(C[0], C[0]);
+#pragma unroll
+      for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(C[k], C[k]));
+      const f32x2 tail = mul2(q, pair(exp2_approx(h.x), exp2_approx(h.y)));
+      const f32x2 minus = mul2(x, pair(-1.f, -1.f));
+      const float2 y = halves(fma2(minus, tail, pair(v[i] < 0.f ? 0.f : v[i],
+                                                     v[i + 1] < 0.f ? 0.f : v[i + 1])));
+      v[i] = y.x;
+      v[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_f<ACT, true>(v[i]);
+  }
+}
+
 // Whether a storage type takes the fast functions.
 template <typename T>
 constexpr bool kFastMath = sizeof(T) == 2;

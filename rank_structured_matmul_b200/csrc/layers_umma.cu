@@ -77,10 +77,13 @@ struct DensePairPolicy {
   // each with a store box of its own (two with Z or a residual): a tile of
   // K = 1024 takes 6 us of MMAs, and one group of four took 13 us over its GELU,
   // bias loads and stores.
-  static constexpr int kEpiWarps = 8;
-  static constexpr int kMaxRegs = 200;  // 320 threads
-  static constexpr uint32_t kGroupBytes = (kKeepZ || kTmaRes ? 2 : 1) * kStoreBoxBytes;
-  static constexpr uint32_t kEpiSmemBytes = 2 * kGroupBytes + 64;  // barriers, a word
+  static constexpr int kEpiWarps = kEpi && !kKeepZ && !kTail ? 16 : 8, kGroups = kEpiWarps / 4;
+  static constexpr int kMaxRegs = kEpiWarps == 16 ? 96 : 200;
+  static constexpr int kCols = kGroups == 4 ? 32 : 64;  // columns of a store box
+  static constexpr uint32_t kBoxBytes = 128u * kCols * 2u;
+  static constexpr int kBufs = kTmaRes && kGroups == 2 ? 2 : 1;  // result boxes of a group
+  static constexpr uint32_t kGroupBytes = (kBufs + (kKeepZ ? 1 : 0)) * kBoxBytes;
+  static constexpr uint32_t kEpiSmemBytes = kGroups * kGroupBytes + 128;  // barriers, a word
 
   static __device__ __forceinline__ void prefetch(const Params& p) {
     tma_prefetch_desc(&p.tmRow);
@@ -132,23 +135,11 @@ struct DensePairPolicy {
     return kColMn ? mnmajor_desc(b, ks) : kmajor_desc(b, ks);
   }
 
-  // 16-byte chunk c of this thread's row in a 64-column store box (128-byte swizzle)
+  // 16-byte chunk c of this thread's row in a store box: rows of 128 or 64 bytes
+  // under the swizzle of that width
   static __device__ __forceinline__ uint4* chunk(uint8_t* box, int row, int c) {
-    return reinterpret_cast<uint4*>(box + row * 128 + ((c ^ (row & 7)) * 16));
-  }
-  // A half box's residual: 8 columns per load, all inside or all beyond M.
-  struct Residual {
-    uint4 q[4];
-  };
-  static __device__ __forceinline__ void fetch(const Params& p, int row, int x, Residual& r) {
-    const size_t at = static_cast<size_t>(row) * p.M + x;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      r.q[c] = make_uint4(0, 0, 0, 0);
-      if (x + c * 8 < p.M && row < p.J &&
-          in_bounds(p.c.status, at + c * 8, 8, static_cast<size_t>(p.J) * p.M))
-        r.q[c] = *reinterpret_cast<const uint4*>(p.residual + at + c * 8);
-    }
+    return reinterpret_cast<uint4*>(kCols == 64 ? box + row * 128 + ((c ^ (row & 7)) * 16)
+                                                : box + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
   }
   static __device__ __forceinline__ float4* part_of(const Params& p, const Tile& t, int part,
                                                     int rank) {
@@ -159,7 +150,7 @@ struct DensePairPolicy {
   static __device__ __forceinline__ bool leave_part(const Params& p, const Tile& t, uint32_t tacc,
                                                     EpiCtx& e) {
     float4* part = part_of(p, t, t.part, e.rank);
-    for (int c = e.group * 32; c < p.bn; c += 64) {
+    for (int c = e.group * 32; c < p.bn; c += 32 * kGroups) {
       __syncwarp();
       uint32_t raw[32];
       tmem_ld_32x32b_x32(tacc + c, raw);
@@ -169,70 +160,68 @@ struct DensePairPolicy {
         part[(c / 4 + q) * 128 + e.row] = make_float4(f32(raw[4 * q]), f32(raw[4 * q + 1]),
                                                       f32(raw[4 * q + 2]), f32(raw[4 * q + 3]));
     }
-    volatile int* last = reinterpret_cast<volatile int*>(e.smem + 2 * kGroupBytes + 48);
+    volatile int* last = reinterpret_cast<volatile int*>(e.smem + kGroups * kGroupBytes + 64);
     __threadfence();
-    named_bar_sync(3, 256);
+    named_bar_sync(kGroups + 1, 32 * kEpiWarps);
     if (e.group == 0 && e.tid == 0) {
       int* counter = p.counters + 2 * t.tail + e.rank;
       const int old = atomicAdd(counter, 1);
       if (old == p.split - 1) *counter = 0;
       *last = old == p.split - 1;
     }
-    named_bar_sync(3, 256);
+    named_bar_sync(kGroups + 1, 32 * kEpiWarps);
     const bool is_last = *last != 0;
-    named_bar_sync(3, 256);  // the word may be written again
+    named_bar_sync(kGroups + 1, 32 * kEpiWarps);  // the word may be written again
     if (is_last) __threadfence();
     return is_last;
   }
-  // raw = the sum of the parts' columns col .. col + 31 of this row, in order
+  // raw = the sum of the parts' columns col .. col + 7 of this row, in order
   static __device__ __forceinline__ void sum_parts(const Params& p, const Tile& t, int col,
-                                                   const EpiCtx& e, uint32_t (&raw)[32]) {
-    float v[32] = {};
-    for (int part = 0; part < p.split; part += 2) {
-      const float4* a = part_of(p, t, part, e.rank) + (col / 4) * 128 + e.row;
-      const float4* b = part_of(p, t, min(part + 1, p.split - 1), e.rank) + (col / 4) * 128 + e.row;
-      float4 x[8], y[8];
+                                                   const EpiCtx& e, uint32_t (&raw)[8]) {
+    float v[8] = {};
+    const float4* from = part_of(p, t, 0, e.rank) + (col / 4) * 128 + e.row;
+    const size_t stride = static_cast<size_t>(2) * (p.bn / 4) * 128;  // from part to part
+    for (int part = 0; part < p.split; part += 4) {
+      float4 x[4][2];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        x[q] = __ldcg(a + q * 128);
-        y[q] = __ldcg(b + q * 128);
+      for (int u = 0; u < 4; ++u) {
+        const float4* at = from + min(part + u, p.split - 1) * stride;
+        x[u][0] = __ldcg(at);
+        x[u][1] = __ldcg(at + 128);
       }
-      const float two = part + 1 < p.split ? 1.f : 0.f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        v[4 * q] += x[q].x, v[4 * q + 1] += x[q].y, v[4 * q + 2] += x[q].z, v[4 * q + 3] += x[q].w;
-        if (two != 0.f) {
-          v[4 * q] += y[q].x, v[4 * q + 1] += y[q].y, v[4 * q + 2] += y[q].z;
-          v[4 * q + 3] += y[q].w;
+      for (int u = 0; u < 4; ++u)
+        if (part + u < p.split) {
+          v[0] += x[u][0].x, v[1] += x[u][0].y, v[2] += x[u][0].z, v[3] += x[u][0].w;
+          v[4] += x[u][1].x, v[5] += x[u][1].y, v[6] += x[u][1].z, v[7] += x[u][1].w;
         }
-      }
     }
 #pragma unroll
-    for (int j = 0; j < 32; ++j) raw[j] = __float_as_uint(v[j]);
+    for (int j = 0; j < 8; ++j) raw[j] = __float_as_uint(v[j]);
   }
-  // Half boxes of 32 columns, one at a time (straight-line code for a whole box
-  // outgrows the instruction cache), the next one's residual in flight.
+  // Eight columns at a time, in a loop: straight-line code for a box of 64 columns
+  // (with the activation some 20 KB) runs out of the instruction caches. The next
+  // columns are on their way from tensor memory meanwhile.
   static __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, uint32_t tacc,
                                                   EpiCtx& e) {
     const bool summed = kTail && t.tail >= 0;
     if (summed && !leave_part(p, t, tacc, e)) return;
     const int y0 = t.j0 + 128 * e.rank, row = y0 + e.row;
-    const int nbox = min(p.bn, p.M - t.m0 + 63) / 64;
+    const int nbox = (min(p.bn, p.M - t.m0) + kCols - 1) / kCols;
     uint8_t* const box = e.smem + e.group * kGroupBytes;
     const uint32_t box_u32 = e.smem_u32 + e.group * kGroupBytes;
     const int bar = 1 + e.group;
-    Residual next;
-    const bool has_r = kKeepZ && p.residual != nullptr;
-    if (has_r && e.group < nbox) fetch(p, row, t.m0 + e.group * 64, next);
+    // kKeepZ: the residual by plain loads, 16 bytes of this thread's row
+    const bool has_r = kKeepZ && p.residual != nullptr && row < p.J;
     // kTmaRes: the group's boxes alternate between its two buffers; a box's
     // residual is on its way while the box before it is finished. The buffers'
     // barriers are made at the group's first box.
-    const uint32_t rbar = e.smem_u32 + 2 * kGroupBytes + e.group * 16u;
+    const uint32_t rbar = e.smem_u32 + kGroups * kGroupBytes + e.group * 16u;
     auto load_residual = [&](int b, uint32_t n) {  // thread 0: box b as the group's n-th
       tma_store_wait_read<0>();                    // the buffer's last store has been read
-      mbar_arrive_expect_tx(rbar + 8u * (n & 1), kStoreBoxBytes);
-      tma_load_2d(box_u32 + (n & 1) * kStoreBoxBytes, &p.tmZ, rbar + 8u * (n & 1), t.m0 + b * 64,
-                  y0);
+      const uint32_t buf = n % kBufs;
+      mbar_arrive_expect_tx(rbar + 8u * buf, kBoxBytes);
+      tma_load_2d(box_u32 + buf * kBoxBytes, &p.tmZ, rbar + 8u * buf, t.m0 + b * kCols, y0);
     };
     if (kTmaRes && e.tid == 0 && e.group < nbox) {
       if (e.counter == 0) {
@@ -243,94 +232,81 @@ struct DensePairPolicy {
       load_residual(e.group, e.counter);
     }
     if (kTmaRes && e.counter == 0) named_bar_sync(bar, 128);  // the barriers exist
-#pragma unroll 1
-    for (int i = 2 * e.group; i < 2 * nbox; i += (i & 1) ? 3 : 1) {
-      const int half = i & 1, col = i * 32, x = t.m0 + (i >> 1) * 64;
-      uint8_t* const dst = box + (kTmaRes ? (e.counter & 1) * kStoreBoxBytes : 0u);
+    uint32_t next[8];
+    if (e.group < nbox && !summed) {
       __syncwarp();
-      uint32_t raw[32];
-      if (summed)
-        sum_parts(p, t, col, e, raw);
-      else
-        tmem_ld_32x32b_x32(tacc + col, raw);
-      uint4 bq[4];
-      if (kEpi && p.bias) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          bq[c] = t.m0 + col + c * 8 < p.M
-                      ? __ldg(reinterpret_cast<const uint4*>(p.bias + t.m0 + col + c * 8))
-                      : make_uint4(0, 0, 0, 0);
-      }
-      const Residual r = next;
-      const int ni = i + (half ? 3 : 1);
-      if (has_r && ni < 2 * nbox) fetch(p, row, t.m0 + ni * 32, next);
-      if (kTmaRes && !half) {
-        if (e.tid == 0 && (i >> 1) + 2 < nbox) load_residual((i >> 1) + 2, e.counter + 1);
-        if (!mbar_wait_until(rbar + 8u * (e.counter & 1), (e.counter >> 1) & 1,
+      tmem_ld_32x32b_x8(tacc + e.group * kCols, next);
+    }
+    for (int b = e.group; b < nbox; b += kGroups) {
+      const int x = t.m0 + b * kCols;
+      uint8_t* const dst = box + (e.counter % kBufs) * kBoxBytes;
+      if (kTmaRes) {
+        if (kBufs > 1 && e.tid == 0 && b + kGroups < nbox) load_residual(b + kGroups, e.counter + 1);
+        if (kBufs == 1 && e.tid == 0 && b != e.group) load_residual(b, e.counter);
+        if (!mbar_wait_until(rbar + 8u * (e.counter % kBufs), (e.counter / kBufs) & 1,
                              globaltimer_ns() + kWaitLimitNs))
           atomicOr(p.c.status, kStatusTimeout);
       }
-      tmem_ld_wait();
-      uint4 y[4], z[4];
+#pragma unroll 1
+      for (int c = 0; c < kCols / 8; ++c) {
+        const int col = x + c * 8;
+        uint4 bq = make_uint4(0, 0, 0, 0), rq = bq;
+        if (kEpi && p.bias && col < p.M) bq = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+        if (has_r && col < p.M) {
+          const size_t at = static_cast<size_t>(row) * p.M + col;
+          if (in_bounds(p.c.status, at, 8, static_cast<size_t>(p.J) * p.M))
+            rq = *reinterpret_cast<const uint4*>(p.residual + at);
+        }
+        if (summed)
+          sum_parts(p, t, b * kCols + c * 8, e, next);
+        else
+          tmem_ld_wait();
+        float v[8];
 #pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = f32(raw[8 * c + j]);
+        for (int j = 0; j < 8; ++j) v[j] = f32(next[j]);
+        if (!summed) {
+          const int nc = (c < kCols / 8 - 1 ? b : b + kGroups - 1) * kCols + c * 8 + 8;
+          __syncwarp();
+          if (nc < nbox * kCols) tmem_ld_32x32b_x8(tacc + nc, next);
+        }
+        uint4 z;
         if (kEpi) {
-          if (p.bias) {
-            add8(v, bq[c]);
-            add8(v + 8, bq[c + 1]);
-          }
-          if (kKeepZ) z[c] = pack8(v), z[c + 1] = pack8(v + 8);
-          // the branch on the activation sits here: around the whole loop it
-          // costs the registers of five loops
-          with_act(p.act, [&](auto tag) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = act_f<decltype(tag)::value, true>(v[j]);
-          });
-          if (kTmaRes) {  // the residual's chunks lie where the result's will
-            add8(v, *chunk(dst, e.row, half * 4 + c));
-            add8(v + 8, *chunk(dst, e.row, half * 4 + c + 1));
-          }
-          if (has_r) {
-            add8(v, r.q[c]);
-            add8(v + 8, r.q[c + 1]);
-          }
+          if (p.bias) add8(v, bq);
+          if (kKeepZ) z = pack8(v);
+          with_act(p.act, [&](auto tag) { act8<decltype(tag)::value>(v); });
+          // the residual's chunk lies where the result's will
+          if (kTmaRes) add8(v, *chunk(dst, e.row, c));
+          if (has_r) add8(v, rq);
         }
-        y[c] = pack8(v), y[c + 1] = pack8(v + 8);
-      }
-      if (!kTmaRes && !half) {  // the box is free once its last store has been read
-        if (e.tid == 0) tma_store_wait_read<0>();
-        named_bar_sync(bar, 128);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        *chunk(dst, e.row, half * 4 + c) = y[c];
-        if (kKeepZ) *chunk(box + kStoreBoxBytes, e.row, half * 4 + c) = z[c];
-      }
-      if (half) {
-        fence_async_shared();
-        named_bar_sync(bar, 128);
-        if (e.tid == 0) {
-          tma_store_2d(&p.tmOut, box_u32 + static_cast<uint32_t>(dst - box), x, y0);
-          if (kKeepZ) tma_store_2d(&p.tmZ, box_u32 + kStoreBoxBytes, x, y0);
-          tma_store_commit();
+        const uint4 y = pack8(v);
+        if (!kTmaRes && c == 0) {  // the box is free once its last store has been read
+          if (e.tid == 0) tma_store_wait_read<0>();
+          named_bar_sync(bar, 128);
         }
-        ++e.counter;
+        *chunk(dst, e.row, c) = y;
+        if (kKeepZ) *chunk(box + kBufs * kBoxBytes, e.row, c) = z;
       }
+      fence_async_shared();
+      named_bar_sync(bar, 128);
+      if (e.tid == 0) {
+        tma_store_2d(&p.tmOut, box_u32 + static_cast<uint32_t>(dst - box), x, y0);
+        if (kKeepZ) tma_store_2d(&p.tmZ, box_u32 + kBufs * kBoxBytes, x, y0);
+        tma_store_commit();
+      }
+      ++e.counter;
     }
   }
   static __device__ __forceinline__ void epilogue_drain(const Params&, EpiCtx& e) { store_drain(e); }
 };
 
-// Tensor map of a stored matrix of `rows` rows of `len` values, in boxes of 64
-// values x box_rows rows.
-bool encode_2d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, uint32_t box_rows) {
+// Tensor map of a stored matrix of `rows` rows of `len` values, in boxes of 64 (or
+// 32) values x box_rows rows, swizzled over the box's row.
+bool encode_2d(CUtensorMap* tm, const void* base, int64_t len, int64_t rows, uint32_t box_rows,
+               uint32_t box_cols = 64) {
   const uint64_t dims[2] = {static_cast<uint64_t>(len), static_cast<uint64_t>(rows)};
   const uint64_t strides[1] = {static_cast<uint64_t>(len) * 2};
-  const uint32_t box[2] = {64, box_rows};
-  return encode_tmap_bf16(tm, base, 2, dims, strides, box, 128);
+  const uint32_t box[2] = {box_cols, box_rows};
+  return encode_tmap_bf16(tm, base, 2, dims, strides, box, static_cast<int>(box_cols * 2));
 }
 
 // How the tiles go over the pairs: where the last round has few tiles, each is
@@ -382,9 +358,9 @@ int launch_pair_as(const LinearGemm& g, int split, const DeviceInfo& dev, cudaSt
       (kRowMn ? encode_2d(&p.tmRow, g.B, g.J, g.K, 64) : encode_2d(&p.tmRow, g.B, g.K, g.J, 128)) &&
       (kColMn ? encode_2d(&p.tmCol, g.A, g.M, g.K, 64)
               : encode_2d(&p.tmCol, g.A, g.K, g.M, static_cast<uint32_t>(p.bn / 2))) &&
-      encode_2d(&p.tmOut, g.Out, g.M, g.J, 128) &&
+      encode_2d(&p.tmOut, g.Out, g.M, g.J, 128, Pol::kCols) &&
       encode_2d(&p.tmZ, kMode == kForwardZ ? g.Z : kMode == kForwardResidual ? g.residual : g.Out,
-                g.M, g.J, 128);
+                g.M, g.J, 128, Pol::kCols);
   if (!ok) return -2;
   const int64_t tiles = static_cast<int64_t>(ceil_div(g.J, 256)) * p.tiles_m;
   if (tiles > 0x7fffffff) return -2;
