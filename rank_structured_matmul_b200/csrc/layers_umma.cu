@@ -73,15 +73,16 @@ struct DensePairPolicy {
     int j0, m0, k0, nk;
     int tail, part;  // tail < 0: a whole tile; nk == 0: nothing
   };
-  // Two groups of four epilogue warps take the tile's 64-column boxes in turn,
-  // each with a store box of its own (two with Z or a residual): a tile of
-  // K = 1024 takes 6 us of MMAs, and one group of four took 13 us over its GELU,
-  // bias loads and stores.
-  static constexpr int kEpiWarps = kEpi && !kKeepZ && !kTail ? 16 : 8, kGroups = kEpiWarps / 4;
+  // Four groups of four epilogue warps take the tile's 32-column store boxes in turn
+  // (two groups and 64-column boxes with Z, whose code needs the registers). A tile of
+  // K = 1024 takes 4.5 us of MMAs; its GELU, bias and stores took one group 13 us, two
+  // groups 8, four 7 (ViT-L fc1 165, 49.3 and 47.0 us in all). A second box per group,
+  // for the residual on its way, pays for the operand stage it costs: 51 -> 48 us.
+  static constexpr int kEpiWarps = kKeepZ ? 8 : 16, kGroups = kEpiWarps / 4;
   static constexpr int kMaxRegs = kEpiWarps == 16 ? 96 : 200;
   static constexpr int kCols = kGroups == 4 ? 32 : 64;  // columns of a store box
   static constexpr uint32_t kBoxBytes = 128u * kCols * 2u;
-  static constexpr int kBufs = kTmaRes && kGroups == 2 ? 2 : 1;  // result boxes of a group
+  static constexpr int kBufs = kTmaRes ? 2 : 1;  // result boxes of a group
   static constexpr uint32_t kGroupBytes = (kBufs + (kKeepZ ? 1 : 0)) * kBoxBytes;
   static constexpr uint32_t kEpiSmemBytes = kGroups * kGroupBytes + 128;  // barriers, a word
 

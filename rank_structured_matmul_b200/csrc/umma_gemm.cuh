@@ -126,7 +126,7 @@ struct EpiCtx {
   int lane;           // lane in warp
   int quad;           // TMEM lane quadrant of this warp
   int tid;            // 0..127 among the epilogue threads (of the group)
-  int group;          // group of four epilogue warps (0 unless EpiWarps is 8)
+  int group;          // group of four epilogue warps (0 unless EpiWarps is above 4)
   uint8_t* smem;      // policy scratch (kEpiSmemBytes), 1024-byte aligned
   uint32_t smem_u32;  // same, as a shared-window address
   uint32_t counter;   // running counter the policy may use (e.g. store buffers)
@@ -155,8 +155,8 @@ struct MaxRegs<Pol, std::void_t<decltype(Pol::kMaxRegs)>> {
   static constexpr int value = Pol::kMaxRegs;
 };
 
-// Epilogue warps of a policy's pair kernel: Pol::kEpiWarps (4 or 8) if it
-// declares them, else 4. Eight are two groups of four, each over all 128 rows.
+// Epilogue warps of a policy's pair kernel: Pol::kEpiWarps (4, 8 or 16) if it
+// declares them, else 4. Each four are a group over all 128 rows.
 template <class Pol, class = void>
 struct EpiWarps {
   static constexpr int value = 4;

@@ -10,7 +10,7 @@
 //    only the leader arms it with the pair's byte count;
 //  - only the leader's warp 1 issues MMAs; completions are committed to the
 //    matching barrier of both CTAs (slot free, accumulator ready);
-//  - both CTAs' epilogue warps (8, or 16 with EpiWarps 8) arrive on the
+//  - both CTAs' epilogue warps (8, or twice EpiWarps) arrive on the
 //    leader's accumulator-free barrier;
 //  - TMEM is allocated and freed pairwise; the cluster synchronises after
 //    set-up and before teardown.
