@@ -42,7 +42,7 @@ struct DensePairParams {
   GemmCommon c;
   CUtensorMap tmRow;  // row operand (J x K, or K x J when MN-major)
   CUtensorMap tmCol;  // column operand (M x K, or K x M when MN-major)
-  CUtensorMap tmOut;  // J x M, box (64, 128), store
+  CUtensorMap tmOut;  // J x M, box (32, 128), store
   CUtensorMap tmZ;    // the same over the kept pre-activations, or the residual
   int J, M, K, bn, tiles_m;
   int act;
@@ -73,14 +73,13 @@ struct DensePairPolicy {
     int j0, m0, k0, nk;
     int tail, part;  // tail < 0: a whole tile; nk == 0: nothing
   };
-  // Four groups of four epilogue warps take the tile's 32-column store boxes in turn
-  // (two groups and 64-column boxes with Z, whose code needs the registers). A tile of
-  // K = 1024 takes 4.5 us of MMAs; its GELU, bias and stores took one group 13 us, two
-  // groups 8, four 7 (ViT-L fc1 165, 49.3 and 47.0 us in all). A second box per group,
-  // for the residual on its way, pays for the operand stage it costs: 51 -> 48 us.
-  static constexpr int kEpiWarps = kKeepZ ? 8 : 16, kGroups = kEpiWarps / 4;
-  static constexpr int kMaxRegs = kEpiWarps == 16 ? 96 : 200;
-  static constexpr int kCols = kGroups == 4 ? 32 : 64;  // columns of a store box
+  // Four groups of four epilogue warps take the tile's 32-column store boxes in turn. A
+  // tile of K = 1024 takes 4.5 us of MMAs; its GELU, bias and stores took one group 13
+  // us, two groups 8, four 7 (ViT-L fc1 165, 49.3 and 47.0 us in all). A second box per
+  // group, for the residual on its way, pays for the operand stage it costs: 51 -> 48 us.
+  static constexpr int kEpiWarps = 16, kGroups = kEpiWarps / 4;
+  static constexpr int kMaxRegs = 96;  // 576 threads
+  static constexpr int kCols = 32;     // columns of a store box
   static constexpr uint32_t kBoxBytes = 128u * kCols * 2u;
   static constexpr int kBufs = kTmaRes ? 2 : 1;  // result boxes of a group
   static constexpr uint32_t kGroupBytes = (kBufs + (kKeepZ ? 1 : 0)) * kBoxBytes;
@@ -136,11 +135,10 @@ struct DensePairPolicy {
     return kColMn ? mnmajor_desc(b, ks) : kmajor_desc(b, ks);
   }
 
-  // 16-byte chunk c of this thread's row in a store box: rows of 128 or 64 bytes
-  // under the swizzle of that width
+  // 16-byte chunk c of this thread's row in a store box (rows of 64 bytes, 64-byte
+  // swizzle)
   static __device__ __forceinline__ uint4* chunk(uint8_t* box, int row, int c) {
-    return reinterpret_cast<uint4*>(kCols == 64 ? box + row * 128 + ((c ^ (row & 7)) * 16)
-                                                : box + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
+    return reinterpret_cast<uint4*>(box + row * 64 + ((c ^ ((row >> 1) & 3)) * 16));
   }
   static __device__ __forceinline__ float4* part_of(const Params& p, const Tile& t, int part,
                                                     int rank) {
@@ -200,9 +198,9 @@ struct DensePairPolicy {
 #pragma unroll
     for (int j = 0; j < 8; ++j) raw[j] = __float_as_uint(v[j]);
   }
-  // Eight columns at a time, in a loop: straight-line code for a box of 64 columns
-  // (with the activation some 20 KB) runs out of the instruction caches. The next
-  // columns are on their way from tensor memory meanwhile.
+  // Eight columns at a time, in a loop: a box in straight-line code is some 20 KB with
+  // the activation and runs out of the instruction caches. The next columns are on
+  // their way from tensor memory meanwhile.
   static __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, uint32_t tacc,
                                                   EpiCtx& e) {
     const bool summed = kTail && t.tail >= 0;
@@ -242,8 +240,7 @@ struct DensePairPolicy {
       const int x = t.m0 + b * kCols;
       uint8_t* const dst = box + (e.counter % kBufs) * kBoxBytes;
       if (kTmaRes) {
-        if (kBufs > 1 && e.tid == 0 && b + kGroups < nbox) load_residual(b + kGroups, e.counter + 1);
-        if (kBufs == 1 && e.tid == 0 && b != e.group) load_residual(b, e.counter);
+        if (e.tid == 0 && b + kGroups < nbox) load_residual(b + kGroups, e.counter + 1);
         if (!mbar_wait_until(rbar + 8u * (e.counter % kBufs), (e.counter / kBufs) & 1,
                              globaltimer_ns() + kWaitLimitNs))
           atomicOr(p.c.status, kStatusTimeout);
