@@ -35,7 +35,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // weight exp(-x^2 / 2) (by linear programming over 4000 points): Phi is off by at
 // most 2.8e-6. An epilogue thread runs 128 of these per 256 x 256 tile. On the
 // ViT-L fc1 forward (40 us without an activation) the GELU with erfcf took 125 us
-// more, with a rational formula of two special-function steps 15.
+// more, with a rational formula of two special-function steps 15, in this form 7.
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -55,10 +55,13 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return FAST ? rcp_approx(1.f + exp2_approx(-kLog2e * z)) : 1.f / (1.f + expf(-z));
 }
 
-// x = min(|z|, 12) (q(x) stays finite, and Phi(-12) = 2e-33 is nothing beside any
-// rounding), e = exp(-x^2 / 2); returns Phi(-x).
+// x = min(|z|, 16), e = exp(-x^2 / 2); returns Phi(-x). At 16 the polynomial is still
+// finite and e is below the smallest normal number, which the instruction flushes to
+// zero: z e is zero for the largest finite z too. (The polynomial is no fit beyond 6,
+// where e < 2e-8 makes its error nothing.)
+constexpr float kPhiMax = 16.f;
 __device__ __forceinline__ float phi_tail_fast(float z, float& x, float& e) {
-  x = fminf(fabsf(z), 12.f);
+  x = fminf(fabsf(z), kPhiMax);
   e = exp2_approx(-0.5f * kLog2e * x * x);
   float q = fmaf(1.85581324e-5f, x, -3.78031295e-4f);
   q = fmaf(q, x, 3.25897020e-3f);
@@ -104,7 +107,9 @@ __device__ __forceinline__ float act_grad_f(float z) {
   }
   if (ACT == DYRA_ACT_GELU_TANH) {
     const float p = sigmoid_f<FAST>(2.f * kTanhC * fmaf(kTanhA * z * z, z, z));
-    const float du = 2.f * kTanhC * fmaf(3.f * kTanhA * z, z, 1.f);  // d(2u)/dz
+    // d(2u)/dz, kept finite: p (1 - p) is zero long before 1e4
+    const float c = fminf(fabsf(z), 1e4f);
+    const float du = 2.f * kTanhC * fmaf(3.f * kTanhA * c, c, 1.f);
     return fmaf(z * p * (1.f - p), du, p);
   }
   if (ACT == DYRA_ACT_SILU) {
@@ -147,7 +152,7 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
                             2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float x0 = fminf(fabsf(v[i]), 12.f), x1 = fminf(fabsf(v[i + 1]), 12.f);
+      const float x0 = fminf(fabsf(v[i]), kPhiMax), x1 = fminf(fabsf(v[i + 1]), kPhiMax);
       const f32x2 x = pair(x0, x1);
       const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
       f32x2 q = pair(C[0], C[0]);
