@@ -18,7 +18,8 @@
  * (its workspace is allocated at creation and never moves, so a captured call
  * may be replayed as long as the handle lives, under the same rule). Weights
  * are arguments of each call, never copied: a training step may change them
- * between calls. Inputs and outputs must not overlap except where said so.
+ * between calls. An output that overlaps an input or another output is refused
+ * (DYRA_ERR_INVALID_ARG) except where said so.
  * No call throws; each returns DYRA_OK or a negative DYRA_ERR_* code and
  * enqueues nothing when it refuses its arguments.
  */
@@ -44,7 +45,7 @@ enum {
 };
 
 /*
- * A dense layer of d_in inputs and d_out outputs (>= 1). DYRA_BF16 needs both
+ * A dense layer of d_in inputs and d_out outputs (1 .. 2^31 - 512). DYRA_BF16 needs both
  * to be multiples of 8 (16-byte rows), else DYRA_ERR_ALIGNMENT. *out is left
  * unchanged on error. The handle owns a workspace of a fixed size (see
  * dyra_dense_device_bytes), whatever the row counts of its calls.

@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "api_util.h"
@@ -44,7 +45,7 @@ struct dyra_moe {
 
 namespace {
 
-// tile origins up to 511 rows beyond the last stay inside 32-bit coordinates
+// of rows and widths: tile origins up to 511 beyond the last stay inside 32-bit coordinates
 constexpr int64_t kMaxRows = (static_cast<int64_t>(1) << 31) - 512;
 
 bool simt_requested() {
@@ -53,6 +54,23 @@ bool simt_requested() {
 }
 
 bool known_act(int act) { return act >= DYRA_ACT_NONE && act <= DYRA_ACT_SILU; }
+
+// The bytes of an argument; a NULL one has none.
+struct Span {
+  uintptr_t at;
+  size_t bytes;
+  Span(const void* p, size_t n) : at(reinterpret_cast<uintptr_t>(p)), bytes(p ? n : 0) {}
+  bool meets(const Span& o) const {
+    return bytes && o.bytes && at < o.at + o.bytes && o.at < at + bytes;
+  }
+  // the same array, or no byte in common
+  bool same_or_apart(const Span& o) const { return at == o.at || !meets(o); }
+};
+bool meets_any(const Span& a, std::initializer_list<Span> others) {
+  for (const Span& o : others)
+    if (a.meets(o)) return true;
+  return false;
+}
 
 // An allocation of the handle, zeroed, counted in its device bytes.
 template <class T>
@@ -152,6 +170,21 @@ int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
                                     static_cast<T*>(p->hidden), p->part, p->status, p->dev, s);
 }
 
+// What the calls on N tokens are given.
+Span rows_of(const dyra_moe* p, const void* a, int64_t N) {
+  return Span(a, elem_size(p->dtype) * N * p->m.d);
+}
+Span slots_of(const dyra_moe* p, const void* a, int64_t N) {  // ids and weights
+  return Span(a, static_cast<size_t>(4) * N * p->m.top_k);
+}
+Span router_of(const dyra_moe* p, const void* Wr) {
+  return Span(Wr, elem_size(p->dtype) * p->m.experts * p->m.d);
+}
+// `halves` 2: gate and up, 1: down
+Span experts_of(const dyra_moe* p, const void* w, int halves) {
+  return Span(w, elem_size(p->dtype) * p->m.experts * halves * p->m.d * p->m.f);
+}
+
 // The shared checks of the calls on N tokens: DYRA_OK to go on.
 int moe_check(const dyra_moe* p, int64_t N) {
   if (p == nullptr || N < 0 || N > kMaxRows) return DYRA_ERR_INVALID_ARG;
@@ -169,6 +202,11 @@ int run_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
   for (const void* q : {X, static_cast<const void*>(ids), static_cast<const void*>(weights), Wgu,
                         Wd, residual, static_cast<const void*>(Y)})
     if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  const Span y = rows_of(p, Y, N);
+  if (meets_any(y, {rows_of(p, X, N), slots_of(p, ids, N), slots_of(p, weights, N),
+                    experts_of(p, Wgu, 2), experts_of(p, Wd, 1)}) ||
+      !y.same_or_apart(rows_of(p, residual, N)))
+    return DYRA_ERR_INVALID_ARG;
   DeviceGuard g(p->dev.device);
   if (!g.ok) return DYRA_ERR_CUDA;
   const size_t row = elem_size(p->dtype) * p->m.d;
@@ -193,7 +231,7 @@ extern "C" {
 int dyra_dense_create(dyra_dense_t* out, int d_in, int d_out, dyra_dtype_t dtype) {
   if (out == nullptr) return DYRA_ERR_INVALID_ARG;
   if (dtype != DYRA_F32 && dtype != DYRA_BF16) return DYRA_ERR_INVALID_ARG;
-  if (d_in < 1 || d_out < 1) return DYRA_ERR_INVALID_ARG;
+  if (d_in < 1 || d_out < 1 || d_in > kMaxRows || d_out > kMaxRows) return DYRA_ERR_INVALID_ARG;
   if (dtype == DYRA_BF16 && (d_in % 8 || d_out % 8)) return DYRA_ERR_ALIGNMENT;
   DeviceInfo dev;
   int rc = current_device_info(&dev);
@@ -227,6 +265,11 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   for (const void* q : {X, W, bias, residual, static_cast<const void*>(Y),
                         static_cast<const void*>(Z)})
     if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  const size_t es = elem_size(p->dtype), out = es * N * p->d_out;
+  const Span x(X, es * N * p->d_in), w(W, es * p->d_out * p->d_in), b(bias, es * p->d_out),
+      r(residual, out), y(Y, out), z(Z, out);
+  if (meets_any(y, {x, w, b, z}) || !y.same_or_apart(r) || meets_any(z, {x, w, b, r}))
+    return DYRA_ERR_INVALID_ARG;
   DeviceGuard dg(p->dev.device);
   if (!dg.ok) return DYRA_ERR_CUDA;
   LinearGemm g;
@@ -257,10 +300,19 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
   for (const void* q : {dY, X, W, Z, static_cast<const void*>(dZ), static_cast<const void*>(dX),
                         static_cast<const void*>(dW), static_cast<const void*>(dbias)})
     if (!aligned16(q)) return DYRA_ERR_ALIGNMENT;
+  const size_t es = elem_size(p->dtype), out = es * N * p->d_out;
+  // what the call reads, and what it writes
+  const Span gy(dY, out), x(dW ? X : nullptr, es * N * p->d_in),
+      w(dX ? W : nullptr, es * p->d_out * p->d_in), z(has_act ? Z : nullptr, out),
+      gz(has_act ? dZ : nullptr, out), gx(dX, es * N * p->d_in), gw(dW, es * p->d_out * p->d_in),
+      gb(dbias, es * p->d_out);
+  if (!gz.same_or_apart(gy) || !gz.same_or_apart(z) || meets_any(gz, {x, w, gx, gw, gb}) ||
+      meets_any(gx, {gy, x, w, z, gw, gb}) || meets_any(gw, {gy, x, w, z, gb}) ||
+      meets_any(gb, {gy, x, w, z}))
+    return DYRA_ERR_INVALID_ARG;
   DeviceGuard dg(p->dev.device);
   if (!dg.ok) return DYRA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t es = elem_size(p->dtype);
   if (N == 0) {
     if ((dW && cudaMemsetAsync(dW, 0, es * p->d_out * p->d_in, s) != cudaSuccess) ||
         (dbias && cudaMemsetAsync(dbias, 0, es * p->d_out, s) != cudaSuccess))
@@ -358,6 +410,10 @@ int dyra_moe_route(dyra_moe_t p, const void* X, const void* Wr, int32_t* ids, fl
     return DYRA_ERR_INVALID_ARG;
   if (!aligned16(X) || !aligned16(Wr) || !aligned16(ids) || !aligned16(weights))
     return DYRA_ERR_ALIGNMENT;
+  const Span i = slots_of(p, ids, N), w = slots_of(p, weights, N);
+  if (meets_any(i, {rows_of(p, X, N), router_of(p, Wr), w}) ||
+      meets_any(w, {rows_of(p, X, N), router_of(p, Wr)}))
+    return DYRA_ERR_INVALID_ARG;
   DeviceGuard g(p->dev.device);
   if (!g.ok) return DYRA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -382,6 +438,11 @@ int dyra_moe_forward(dyra_moe_t p, const void* X, const void* Wr, const void* Wg
   if (Wgu == nullptr || Wd == nullptr || Y == nullptr) return DYRA_ERR_INVALID_ARG;
   if (!aligned16(Wgu) || !aligned16(Wd) || !aligned16(residual) || !aligned16(Y))
     return DYRA_ERR_ALIGNMENT;
+  const Span y = rows_of(p, Y, N), r = rows_of(p, residual, N), i = slots_of(p, ids, N),
+             w = slots_of(p, weights, N), gu = experts_of(p, Wgu, 2), dn = experts_of(p, Wd, 1);
+  if (meets_any(y, {rows_of(p, X, N), router_of(p, Wr), i, w, gu, dn}) || !y.same_or_apart(r) ||
+      meets_any(i, {gu, dn, r}) || meets_any(w, {gu, dn, r}))
+    return DYRA_ERR_INVALID_ARG;
   rc = dyra_moe_route(p, X, Wr, ids, weights, N, stream);
   if (rc) return rc;
   return run_experts(p, X, ids, weights, Wgu, Wd, residual, Y, N,

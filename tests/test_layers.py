@@ -751,3 +751,129 @@ def test_bf16_on_the_cuda_cores(N, monkeypatch):
     check_backward(layer, X, W, Z, R, "gelu", "bf16")
     layer.close()
     check_moe(min(N, 64), 136, 72, 9, 3, "bf16", True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_activations_far_out(act, dtype):
+    """Beyond |z| = 100 the activations are z or 0 and their slopes 1 or 0 to less
+    than 1e-40, up to the largest finite values, and a NaN stays one."""
+    z = torch.tensor([100.0, 1e4, 3e9, 2e19, 1e25, 2e30, 3e38, -100.0, -1e4, -3e9, -2e19, -1e25,
+                      -2e30, -3e38, float("nan"), 0.0], device="cuda", dtype=DT[dtype])
+    n = z.numel()
+    layer = layers.DenseLinear(8, n, dtype)
+    X = torch.zeros(1, 8, device="cuda", dtype=DT[dtype])
+    W = torch.zeros(n, 8, device="cuda", dtype=DT[dtype])
+    Y = layer.forward(X, W, bias=z, act=act)[0]
+    ones = torch.ones(1, n, device="cuda", dtype=DT[dtype])
+    _, _, slope = layer.backward(ones, None, None, Z=z.view(1, n), act=act, need_dX=False,
+                                 need_dW=False)
+    assert torch.isnan(Y[14]) and torch.isnan(slope[14])
+    assert Y[15] == 0.0 and slope[15] == 0.5
+    assert torch.equal(Y[:7], z[:7]) and bool((Y[7:14].abs() < 1e-37).all())
+    assert bool((slope[:7] == 1.0).all()) and bool((slope[7:14].abs() < 1e-37).all())
+    layer.close()
+
+
+def test_overlapping_outputs_are_refused():
+    n, d = 16, 64
+    layer, moe = layers.DenseLinear(d, d), layers.MoeLayer(d, d, 4, 2)
+    X, W, b, R = dense_case(n, d, d, "bf16")
+    _, Wr, Wgu, Wd, _ = moe_case(n, d, d, 4, 2, "bf16")
+    Y, Z, G, V = (torch.full((n, d), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    big = torch.full((2 * n, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    ids = torch.zeros(n, 2, device="cuda", dtype=torch.int32)
+    w = torch.zeros(n, 2, device="cuda")
+    kept = [t.clone() for t in (X, W, b, R, Wr, Wgu, Wd, ids, w)]
+    s = torch.cuda.current_stream().cuda_stream
+
+    def refused(call, handle, *a):
+        with pytest.raises(dyra.DyraError) as e:
+            call(handle, *a)
+        assert e.value.code == dyra.DYRA_ERR_INVALID_ARG
+
+    fwd, bwd = layers.dyra_dense_forward, layers.dyra_dense_backward
+    h, gelu = layer.handle, layers.DYRA_ACT_GELU
+    for y in (X, W, b, Z):
+        refused(fwd, h, X, W, b, R, gelu, y, Z, n, s)
+    for z in (X, W, b, R):
+        refused(fwd, h, X, W, b, R, gelu, Y, z, n, s)
+    refused(fwd, h, X, W, b, big[:n], gelu, big[1:n + 1], None, n, s)  # not the same rows
+    refused(fwd, h, big[:n], W, b, R, gelu, big[n - 1:2 * n - 1], None, n, s)
+    for dz in (X, W, b):
+        refused(bwd, h, R, X, W, Z, gelu, dz, Y, G, b if dz is not b else dz, n, s)
+    refused(bwd, h, R, X, W, big[:n], gelu, big[2:n + 2], Y, G, b, n, s)
+    for over in (R, X, W, Z, V, G, b):
+        refused(bwd, h, R, X, W, Z, gelu, V, over, G, b, n, s)
+    for over in (R, X, W, Z, V, b):
+        refused(bwd, h, R, X, W, Z, gelu, V, Y, over, b, n, s)
+    for over in (R, X, W, Z, V):
+        refused(bwd, h, R, X, W, Z, gelu, V, Y, G, over, n, s)
+    h = moe.handle
+    for y in (X, ids, w, Wgu, Wd):
+        refused(layers.dyra_moe_experts, h, X, ids, w, Wgu, Wd, R, y, n, s)
+        refused(layers.dyra_moe_forward, h, X, Wr, Wgu, Wd, R, y, ids, w, n, s)
+    refused(layers.dyra_moe_forward, h, X, Wr, Wgu, Wd, R, Wr, ids, w, n, s)
+    refused(layers.dyra_moe_experts, h, X, ids, w, Wgu, Wd, big[:n], big[1:n + 1], n, s)
+    for over in (X, Wr, ids):
+        refused(layers.dyra_moe_route, h, X, Wr, ids, over, n, s)
+    for over in (X, Wr, w):
+        refused(layers.dyra_moe_route, h, X, Wr, over, w, n, s)
+    for over in (Wgu, Wd, R):
+        refused(layers.dyra_moe_forward, h, X, Wr, Wgu, Wd, R, Y, over, w, n, s)
+        refused(layers.dyra_moe_forward, h, X, Wr, Wgu, Wd, R, Y, ids, over, n, s)
+    torch.cuda.synchronize()
+    for t, k in zip((X, W, b, R, Wr, Wgu, Wd, ids, w), kept):
+        assert torch.equal(t, k)
+    assert bool((Y == 7.0).all()) and bool((big == 7.0).all())
+    # what is not read may be written over: X without dW, Z and dZ without an activation
+    z0 = torch.zeros(n, d, device="cuda", dtype=torch.bfloat16)
+    bwd(layer.handle, R, z0, W, z0, 0, z0, z0, None, None, n, s)
+    dX, _, _ = layer.backward(R, None, W, need_dW=False, need_dbias=False)
+    assert torch.equal(z0, dX)
+    assert layer.status() == 0 and moe.status() == 0
+    layer.close(), moe.close()
+
+
+@pytest.mark.parametrize("graphs", ["0", "1"])
+def test_between_approximated_layers(graphs, monkeypatch):
+    """Exact layers before and behind an approximated one whose factors change from
+    step to step, all on one stream without a wait: the bits of the same calls with
+    a wait after each."""
+    monkeypatch.setenv("DYRA_GRAPHS", graphs)
+    B, T, d, f, r, k = 3, 67, 256, 512, 64, 32
+    up, down = layers.DenseLinear(d, f), layers.DenseLinear(d, d)
+    mid = dyra.DyraLinear(f, d, r, k)
+    X, W1, b1, _ = dense_case(B * T, d, f, "bf16", seed=3)
+    _, W2, b2, _ = dense_case(B * T, d, d, "bf16", seed=4)
+    g = gen(5)
+    factors = [(rand(g, d, r, scale=r ** -0.5), rand(g, f, r, scale=f ** -0.5),
+                rand(g, f, k, scale=f ** -0.5), rand(g, d, f, scale=0.1 * f ** -0.5))
+               for _ in range(2)]
+    h, y = X.new_empty(B * T, f), X.new_empty(B * T, d)
+    s = torch.cuda.Stream()
+
+    def chain(wait):
+        x, out = X.clone(), []
+        for i in range(6):
+            dyra.dyra_load_factors(mid.plan, *factors[i % 2], 0.1, s)
+            wait()
+            up.forward(x, W1, bias=b1, act="gelu", Y=h, stream=s)
+            wait()
+            mid.forward(h, B=B, T=T, Y=y, stream=s)
+            wait()
+            z = down.forward(y, W2, bias=b2, residual=x, act="silu", stream=s)
+            wait()
+            x.copy_(z / z.float().std().to(z.dtype))
+            wait()
+            out.append(x.clone())
+        return out
+
+    with torch.cuda.stream(s):
+        want = chain(torch.cuda.synchronize)
+        assert all(bool(torch.isfinite(t).all()) for t in want)
+        for _ in range(3):
+            for a, c in zip(chain(lambda: None), want):
+                assert torch.equal(a, c)
+    assert up.status() == 0 and down.status() == 0 and mid.status() == 0
+    up.close(), down.close(), mid.close()

@@ -18,6 +18,8 @@ F32, BF16 = dyra.DYRA_F32, dyra.DYRA_BF16
     ((64, 64, 2), INV),       # unknown type
     ((60, 64, BF16), ALIGN),  # d_in % 8
     ((64, 60, BF16), ALIGN),  # d_out % 8
+    ((2 ** 31 - 504, 64, BF16), INV),  # beyond 2^31 - 512
+    ((64, 2 ** 31 - 511, F32), INV),
 ])
 def test_dense_create_rejects(args, code):
     h = ctypes.c_void_p()
