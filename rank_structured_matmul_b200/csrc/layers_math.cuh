@@ -142,23 +142,30 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   return d;
 }
 
+// Phi(-|z|) of two values (phi_tail_fast): x = min(|z|, kPhiMax) and e = exp(-x^2 / 2)
+// too.
+__device__ __forceinline__ f32x2 phi_tail2(float z0, float z1, f32x2& x, f32x2& e) {
+  constexpr float C[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
+                          -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
+                          2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
+  x = pair(fminf(fabsf(z0), kPhiMax), fminf(fabsf(z1), kPhiMax));
+  const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
+  e = pair(exp2_approx(h.x), exp2_approx(h.y));
+  f32x2 q = pair(C[0], C[0]);
+#pragma unroll
+  for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(C[k], C[k]));
+  return mul2(q, e);
+}
+
 // act_f<ACT, true> of eight values; the GELU's polynomial two values at a time,
 // which nearly halves its instructions.
 template <int ACT>
 __device__ __forceinline__ void act8(float (&v)[8]) {
   if constexpr (ACT == DYRA_ACT_GELU) {
-    constexpr float C[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
-                            -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
-                            2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float x0 = fminf(fabsf(v[i]), kPhiMax), x1 = fminf(fabsf(v[i + 1]), kPhiMax);
-      const f32x2 x = pair(x0, x1);
-      const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
-      f32x2 q = pair(C[0], C[0]);
-#pragma unroll
-      for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(C[k], C[k]));
-      const f32x2 tail = mul2(q, pair(exp2_approx(h.x), exp2_approx(h.y)));
+      f32x2 x, e;
+      const f32x2 tail = phi_tail2(v[i], v[i + 1], x, e);
       const f32x2 minus = mul2(x, pair(-1.f, -1.f));
       const float2 y = halves(fma2(minus, tail, pair(v[i] < 0.f ? 0.f : v[i],
                                                      v[i + 1] < 0.f ? 0.f : v[i + 1])));
@@ -168,6 +175,27 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act_f<ACT, true>(v[i]);
+  }
+}
+
+// act_grad_f<ACT, true> of eight values, in the same way.
+template <int ACT>
+__device__ __forceinline__ void act_grad8(float (&v)[8]) {
+  if constexpr (ACT == DYRA_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      f32x2 x, e;
+      const float2 tail = halves(phi_tail2(v[i], v[i + 1], x, e));
+      const f32x2 phi = pair(v[i] < 0.f ? tail.x : 1.f - tail.x,
+                             v[i + 1] < 0.f ? tail.y : 1.f - tail.y);
+      const float2 y = halves(fma2(mul2(pair(v[i], v[i + 1]), pair(kInvSqrt2Pi, kInvSqrt2Pi)), e,
+                                   phi));
+      v[i] = y.x;
+      v[i + 1] = y.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = act_grad_f<ACT, true>(v[i]);
   }
 }
 
