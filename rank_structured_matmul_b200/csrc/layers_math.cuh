@@ -60,17 +60,18 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 // zero: z e is zero for the largest finite z too. (The polynomial is no fit beyond 6,
 // where e < 2e-8 makes its error nothing.)
 constexpr float kPhiMax = 16.f;
-__device__ __forceinline__ float phi_tail_fast(float z, float& x, float& e) {
+__device__ __forceinline__ float phi_poly(int k) {
+  constexpr float c[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
+                          -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
+                          2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
+  return c[k];
+}
+__device__ __forceinline__ float phi_tail_fast(float z, float& x) {
   x = fminf(fabsf(z), kPhiMax);
-  e = exp2_approx(-0.5f * kLog2e * x * x);
-  float q = fmaf(1.85581324e-5f, x, -3.78031295e-4f);
-  q = fmaf(q, x, 3.25897020e-3f);
-  q = fmaf(q, x, -1.60708737e-2f);
-  q = fmaf(q, x, 5.25960136e-2f);
-  q = fmaf(q, x, -1.27570483e-1f);
-  q = fmaf(q, x, 2.48509570e-1f);
-  q = fmaf(q, x, -3.98784939e-1f);
-  q = fmaf(q, x, 4.99997257e-1f);
+  const float e = exp2_approx(-0.5f * kLog2e * x * x);
+  float q = phi_poly(0);
+#pragma unroll
+  for (int k = 1; k < 9; ++k) q = fmaf(q, x, phi_poly(k));
   return q * e;
 }
 
@@ -80,8 +81,8 @@ __device__ __forceinline__ float act_f(float z) {
   if (ACT == DYRA_ACT_RELU) return relu;
   if (ACT == DYRA_ACT_GELU) {
     if (!FAST) return z * (0.5f * erfcf(-z * kSqrtHalf));  // erfc: exact for z << 0
-    float x, e;
-    const float tail = phi_tail_fast(z, x, e);
+    float x;
+    const float tail = phi_tail_fast(z, x);
     return fmaf(-x, tail, relu);  // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
   }
   if (ACT == DYRA_ACT_GELU_TANH)  // (1 + tanh u) / 2 = sigmoid(2 u)
@@ -94,15 +95,8 @@ template <int ACT, bool FAST = false>
 __device__ __forceinline__ float act_grad_f(float z) {
   if (ACT == DYRA_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (ACT == DYRA_ACT_GELU) {
-    float phi, e;
-    if (FAST) {
-      float x;
-      const float tail = phi_tail_fast(z, x, e);
-      phi = z < 0.f ? tail : 1.f - tail;
-    } else {
-      e = expf(-0.5f * z * z);
-      phi = 0.5f * erfcf(-z * kSqrtHalf);
-    }
+    static_assert(!FAST || ACT != DYRA_ACT_GELU, "act_grad8");
+    const float e = expf(-0.5f * z * z), phi = 0.5f * erfcf(-z * kSqrtHalf);
     return fmaf(z * kInvSqrt2Pi, e, phi);
   }
   if (ACT == DYRA_ACT_GELU_TANH) {
@@ -145,15 +139,12 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
 // Phi(-|z|) of two values (phi_tail_fast): x = min(|z|, kPhiMax) and e = exp(-x^2 / 2)
 // too.
 __device__ __forceinline__ f32x2 phi_tail2(float z0, float z1, f32x2& x, f32x2& e) {
-  constexpr float C[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
-                          -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
-                          2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
   x = pair(fminf(fabsf(z0), kPhiMax), fminf(fabsf(z1), kPhiMax));
   const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
   e = pair(exp2_approx(h.x), exp2_approx(h.y));
-  f32x2 q = pair(C[0], C[0]);
+  f32x2 q = pair(phi_poly(0), phi_poly(0));
 #pragma unroll
-  for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(C[k], C[k]));
+  for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(phi_poly(k), phi_poly(k)));
   return mul2(q, e);
 }
 
@@ -178,7 +169,7 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
   }
 }
 
-// act_grad_f<ACT, true> of eight values, in the same way.
+// The slopes of eight values, fast, in the same way.
 template <int ACT>
 __device__ __forceinline__ void act_grad8(float (&v)[8]) {
   if constexpr (ACT == DYRA_ACT_GELU) {

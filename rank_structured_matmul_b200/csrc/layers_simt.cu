@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(256, kActBlocks<ACT>)
             act_grad8<ACT>(slope);
           } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) slope[i] = act_grad_f<ACT, kFastMath<T>>(slope[i]);
+            for (int i = 0; i < V; ++i) slope[i] = act_grad_f<ACT>(slope[i]);
           }
         }
 #pragma unroll
@@ -492,10 +492,11 @@ int launch_act_backward(const T* dY, const T* Z, int act, T* dZ, T* dbias, int64
                         float* partial, int* counters, int* status, const DeviceInfo& dev,
                         cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  if (d_out % V == 0)
-    return launch_act_backward_v<T, V>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
-                                       dev, s);
-  return launch_act_backward_v<T, 1>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
+  if constexpr (sizeof(T) == 4)  // (bf16 rows are whole 16-byte pieces)
+    if (d_out % V)
+      return launch_act_backward_v<T, 1>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
+                                         dev, s);
+  return launch_act_backward_v<T, V>(dY, Z, act, dZ, dbias, N, d_out, partial, counters, status,
                                      dev, s);
 }
 template int launch_act_backward<float>(const float*, const float*, int, float*, float*, int64_t,
