@@ -13,7 +13,6 @@ results are allocated too.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional
 
@@ -154,12 +153,14 @@ class _Layer:
 
     def _new(self, like, on, *shapes):
         """New tensors of the layer's type (None for a shape of None), allocated on
-        the call's stream."""
+        the call's stream. (Sizes as arguments: as one tuple they take new_empty half
+        as long again, 1.9 us instead of 1.4.)"""
         if on is not None:
             import torch
             with torch.cuda.stream(on):
-                return [like.new_empty(s) if s else None for s in shapes]
-        return [like.new_empty(s) if s else None for s in shapes]
+                return self._new(like, None, *shapes)
+        new = like.new_empty
+        return [new(*s) if s else None for s in shapes]
 
     def __del__(self):
         try:
@@ -253,10 +254,12 @@ class MoeLayer(_Layer):
         return N
 
     def _new_routing(self, X, on, N):
-        import torch
-        with torch.cuda.stream(on) if on is not None else contextlib.nullcontext():
-            return (X.new_empty((N, self.top_k), dtype=self.int32),
-                    X.new_empty((N, self.top_k), dtype=self.float32))
+        if on is not None:
+            import torch
+            with torch.cuda.stream(on):
+                return self._new_routing(X, None, N)
+        return (X.new_empty(N, self.top_k, dtype=self.int32),
+                X.new_empty(N, self.top_k, dtype=self.float32))
 
     def route(self, X, Wr, stream=None):
         """(ids, weights): each token's top_k experts, largest logit first (the
