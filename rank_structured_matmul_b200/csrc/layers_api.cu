@@ -26,6 +26,7 @@ struct dyra_dense {
   int* tiles = nullptr;     // their arrival counters, zero between calls
   int n_tiles = 0;
   int* status = nullptr;
+  void* base = nullptr;     // the one allocation that holds them
   size_t bytes = 0;
 };
 
@@ -39,6 +40,7 @@ struct dyra_moe {
   double* logits = nullptr;  // the router's
   int* tiles = nullptr;    // arrival counters, zero between calls: the router's, then the tiles'
   int* status = nullptr;
+  void* base = nullptr;    // the one allocation that holds them
   size_t bytes = 0;
   int n_tiles = 0;
 };
@@ -72,28 +74,30 @@ bool meets_any(const Span& a, std::initializer_list<Span> others) {
   return false;
 }
 
-// An allocation of the handle, zeroed, counted in its device bytes.
+// A handle's buffers are parts of one allocation (a bf16 dense handle takes 0.05 ms to
+// make, with an allocation per buffer 0.13). Those that begin at zero come first.
+struct Layout {
+  size_t total = 0;
+  size_t add(size_t bytes) {
+    const size_t at = total;
+    total += (bytes + 255) & ~static_cast<size_t>(255);
+    return at;
+  }
+};
 template <class T>
-int take(T** p, size_t bytes, size_t* total) {
-  void* v = nullptr;
-  const size_t rounded = (bytes + 255) & ~static_cast<size_t>(255);
-  const int rc = dev_alloc(&v, rounded);
+T* part_at(void* base, size_t at) {
+  return reinterpret_cast<T*>(static_cast<char*>(base) + at);
+}
+int allocate(void** base, const Layout& l, size_t zeroed) {
+  const int rc = dev_alloc(base, l.total);
   if (rc) return rc;
-  *p = static_cast<T*>(v);
-  *total += rounded;
   // done before any stream can use the handle
-  if (cudaMemset(v, 0, rounded) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+  if (cudaMemset(*base, 0, zeroed) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
     cudaGetLastError();
+    dev_free(*base);
     return DYRA_ERR_CUDA;
   }
   return DYRA_OK;
-}
-
-template <class T>
-void give(T*& p) {
-  void* v = p;
-  dev_free(v);
-  p = nullptr;
 }
 
 // A call that gave up may leave arrival counters behind: they start again.
@@ -103,7 +107,7 @@ int read_status(const DeviceInfo& dev, int* status, int* tiles, int n_tiles) {
   int st = 0;
   if (cudaMemcpy(&st, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
       cudaMemset(status, 0, sizeof(int)) != cudaSuccess ||
-      (st != 0 && tiles && cudaMemset(tiles, 0, sizeof(int) * n_tiles) != cudaSuccess) ||
+      (st != 0 && n_tiles && cudaMemset(tiles, 0, sizeof(int) * n_tiles) != cudaSuccess) ||
       cudaStreamSynchronize(nullptr) != cudaSuccess)
     return DYRA_ERR_CUDA;
   return st;
@@ -127,24 +131,6 @@ int act_backward(const dyra_dense* p, const void* dY, const void* Z, int act, vo
   return launch_act_backward<T>(static_cast<const T*>(dY), static_cast<const T*>(Z), act,
                                 static_cast<T*>(dZ), static_cast<T*>(dbias), N, p->d_out,
                                 p->colsum, p->counters, p->status, p->dev, s);
-}
-
-void dense_free(dyra_dense* p) {
-  give(p->colsum);
-  give(p->counters);
-  give(p->ws);
-  give(p->tiles);
-  give(p->status);
-  delete p;
-}
-
-void moe_free(dyra_moe* p) {
-  give(p->hidden);
-  give(p->part);
-  give(p->logits);
-  give(p->tiles);
-  give(p->status);
-  delete p;
 }
 
 template <class T>
@@ -244,14 +230,21 @@ int dyra_dense_create(dyra_dense_t* out, int d_in, int d_out, dyra_dtype_t dtype
   p->dev = dev;
   p->simt = dtype == DYRA_F32 || simt_requested();
   p->n_tiles = p->simt ? 0 : linear_counters(dev);
-  if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
-      (rc = take(&p->colsum, sizeof(float) * kColSumChunks * d_out, &p->bytes)) ||
-      (rc = take(&p->counters, sizeof(int) * col_sum_blocks(d_out), &p->bytes)) ||
-      (!p->simt && (rc = take(&p->ws, linear_ws_bytes(dev), &p->bytes))) ||
-      (!p->simt && (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes)))) {
-    dense_free(p);
+  Layout l;
+  const size_t status = l.add(sizeof(int)), counters = l.add(sizeof(int) * col_sum_blocks(d_out)),
+               tiles = l.add(sizeof(int) * p->n_tiles), zeroed = l.total,
+               colsum = l.add(sizeof(float) * kColSumChunks * d_out),
+               ws = l.add(p->simt ? 0 : linear_ws_bytes(dev));
+  if ((rc = allocate(&p->base, l, zeroed))) {
+    delete p;
     return rc;
   }
+  p->bytes = l.total;
+  p->status = part_at<int>(p->base, status);
+  p->counters = part_at<int>(p->base, counters);
+  p->tiles = part_at<int>(p->base, tiles);
+  p->colsum = part_at<float>(p->base, colsum);
+  p->ws = part_at<float>(p->base, ws);
   *out = p;
   return DYRA_OK;
 }
@@ -362,7 +355,8 @@ int dyra_dense_destroy(dyra_dense_t p) {
   if (p == nullptr) return DYRA_OK;
   DeviceGuard g(p->dev.device);
   cudaDeviceSynchronize();
-  dense_free(p);
+  dev_free(p->base);
+  delete p;
   return DYRA_OK;
 }
 
@@ -390,14 +384,20 @@ int dyra_moe_create(dyra_moe_t* out, int d_model, int d_ff, int experts, int top
       p->simt ? slots : static_cast<size_t>(kMoeTokens) * moe_reached_max(p->m);
   const size_t part_bytes = p->simt ? slots * d_model * sizeof(float) : moe_ws_bytes(p->m, dev);
   p->n_tiles = moe_route_counters() + (p->simt ? 0 : moe_counters(p->m));
-  if ((rc = take(&p->status, sizeof(int), &p->bytes)) ||
-      (rc = take(&p->hidden, hidden_rows * d_ff * elem_size(dtype), &p->bytes)) ||
-      (rc = take(&p->part, part_bytes, &p->bytes)) ||
-      (rc = take(&p->logits, moe_logit_bytes(p->m), &p->bytes)) ||
-      (rc = take(&p->tiles, sizeof(int) * p->n_tiles, &p->bytes))) {
-    moe_free(p);
+  Layout l;
+  const size_t status = l.add(sizeof(int)), tiles = l.add(sizeof(int) * p->n_tiles),
+               zeroed = l.total, hidden = l.add(hidden_rows * d_ff * elem_size(dtype)),
+               part = l.add(part_bytes), logits = l.add(moe_logit_bytes(p->m));
+  if ((rc = allocate(&p->base, l, zeroed))) {
+    delete p;
     return rc;
   }
+  p->bytes = l.total;
+  p->status = part_at<int>(p->base, status);
+  p->tiles = part_at<int>(p->base, tiles);
+  p->hidden = part_at<char>(p->base, hidden);
+  p->part = part_at<float>(p->base, part);
+  p->logits = part_at<double>(p->base, logits);
   *out = p;
   return DYRA_OK;
 }
@@ -459,7 +459,8 @@ int dyra_moe_destroy(dyra_moe_t p) {
   if (p == nullptr) return DYRA_OK;
   DeviceGuard g(p->dev.device);
   cudaDeviceSynchronize();
-  moe_free(p);
+  dev_free(p->base);
+  delete p;
   return DYRA_OK;
 }
 
