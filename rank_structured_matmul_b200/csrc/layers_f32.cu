@@ -520,12 +520,12 @@ int launch_linear_f32(const LinearGemm& g, const DeviceInfo& dev, cudaStream_t s
 int launch_moe_tiles_f32(const MoeShape& m, const float* X, const int* ids, const float* Wgu,
                          const float* Wd, int N, float* hidden, float* part, int* status,
                          const DeviceInfo& dev, cudaStream_t s) {
-  const bool vec = m.d % 4 == 0 && m.f % 4 == 0;  // rows of whole 16-byte pieces
-  if (vec ? launch_experts<0, true>(m, X, ids, Wgu, hidden, N, status, dev, s)
-          : launch_experts<0, false>(m, X, ids, Wgu, hidden, N, status, dev, s))
+  // a stage's rows are whole 16-byte pieces: of d values in the first, f in the second
+  if (m.d % 4 ? launch_experts<0, false>(m, X, ids, Wgu, hidden, N, status, dev, s)
+              : launch_experts<0, true>(m, X, ids, Wgu, hidden, N, status, dev, s))
     return -1;
-  return vec ? launch_experts<1, true>(m, hidden, ids, Wd, part, N, status, dev, s)
-             : launch_experts<1, false>(m, hidden, ids, Wd, part, N, status, dev, s);
+  return m.f % 4 ? launch_experts<1, false>(m, hidden, ids, Wd, part, N, status, dev, s)
+                 : launch_experts<1, true>(m, hidden, ids, Wd, part, N, status, dev, s);
 }
 
 }  // namespace dyra

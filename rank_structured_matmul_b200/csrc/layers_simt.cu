@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(256)
 // per output row of one expert, over the slots (token, k) that name it, up to eight at
 // a time: each weight is read once per eight slots. STAGE 0: hidden[slot] = act(g) u
 // over rows f; STAGE 1: part[slot] over rows d. The slots of the block's expert are
-// listed in order first. VEC: the rows are whole 16-byte pieces. A warp's time is the
+// listed in order first. VEC: the stage's rows are whole 16-byte pieces. A warp's time is the
 // latency of its loads; two rows per warp, for half the loads of x, were slower (151
 // against 94 us for 14 tokens on 5 experts of 601 x 1935).
 
@@ -544,9 +544,9 @@ int launch_moe_experts_simt(const MoeShape& m, const T* X, const int* ids, const
     if (tiles && launch_moe_tiles_f32(m, X, ids, Wgu, Wd, N, hidden, part, status, dev, s)) return -1;
   }
   if (!tiles) {
-    const bool vec = m.d * sizeof(T) % 16 == 0 && m.f * sizeof(T) % 16 == 0;
-    auto up = vec ? moe_expert_kernel<T, 0, true> : moe_expert_kernel<T, 0, false>;
-    auto down = vec ? moe_expert_kernel<T, 1, true> : moe_expert_kernel<T, 1, false>;
+    // a stage's rows are whole 16-byte pieces: of d values in the first, f in the second
+    auto up = m.d * sizeof(T) % 16 ? moe_expert_kernel<T, 0, false> : moe_expert_kernel<T, 0, true>;
+    auto down = m.f * sizeof(T) % 16 ? moe_expert_kernel<T, 1, false> : moe_expert_kernel<T, 1, true>;
     if (launch_dependent(up, dim3((m.f + 7) / 8, m.experts), dim3(256), 0, 1, s, m, X, ids, Wgu,
                          hidden, static_cast<float*>(nullptr), N, status) ||
         launch_dependent(down, dim3((m.d + 7) / 8, m.experts), dim3(256), 0, 1, s, m,

@@ -490,8 +490,9 @@ MOE_BF16 = [(1, 64, 64, 4, 1), (1, 512, 1024, 8, 2), (2, 128, 72, 8, 8), (3, 100
             (7, 136, 200, 64, 4), (16, 256, 512, 8, 2), (17, 264, 136, 5, 2), (33, 2048, 128, 9, 3),
             (64, 512, 256, 128, 8), (64, 8, 8, 3, 3), (1, 4096, 2048, 2, 2), (48, 72, 1032, 300, 16),
             (33, 16, 24, 512, 16), (5, 1288, 8, 3, 1), (40, 8, 2056, 2, 2)]
-MOE_F32 = [(1, 1, 1, 1, 1), (50, 136, 200, 3, 2), (61, 33, 70, 2, 2), (64, 5, 129, 1, 1), (3, 256, 512, 8, 2), (5, 33, 17, 6, 3), (64, 65, 70, 12, 4),
-           (2, 1000, 251, 4, 2)]
+MOE_F32 = [(1, 1, 1, 1, 1), (50, 136, 200, 3, 2), (61, 33, 70, 2, 2), (64, 5, 129, 1, 1),
+           (3, 256, 512, 8, 2), (5, 33, 17, 6, 3), (64, 65, 70, 12, 4), (2, 1000, 251, 4, 2),
+           (3, 133, 264, 5, 3), (50, 133, 264, 3, 2), (50, 132, 261, 3, 2)]
 
 
 @pytest.mark.parametrize("renorm", [True, False])
