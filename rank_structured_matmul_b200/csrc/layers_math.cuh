@@ -28,14 +28,20 @@ constexpr float kTanhA = 0.044715f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Two accuracies of each function. FAST serves the bf16 layers, whose results
-// are rounded to 2^-8 of themselves at best: the hardware's approximate 2^x and
+// are rounded to 2^-8 of themselves: the hardware's approximate 2^x and
 // reciprocal (about 2^-22), and for the normal distribution
-//   Phi(-x) = exp(-x^2 / 2) q(x),  q(x) = erfcx(x / sqrt 2) / 2, x >= 0,
-// with q a polynomial of degree 8, the minimax fit of q on [0, 6] under the
-// weight exp(-x^2 / 2) (by linear programming over 4000 points): Phi is off by at
-// most 2.8e-6. An epilogue thread runs 128 of these per 256 x 256 tile. On the
-// ViT-L fc1 forward (40 us without an activation) the GELU with erfcf took 125 us
-// more, with a rational formula of two special-function steps 15, in this form 7.
+//   Phi(-x) = 2^P(x), x >= 0,
+// with P a polynomial of degree 10. log2 Phi(-x) is nearly a parabola, so the
+// tail keeps its relative accuracy where a polynomial of that degree times
+// exp(-x^2 / 2) loses it. P is fitted by linear programming over 3000 points of
+// [0, 13.05] so that the largest of |error of Phi| / 4e-7 and |error of Phi| /
+// (2^-12 Phi) is least. Evaluated in fp32, Phi(-x) is off by at most 3.4e-7 and by
+// at most 2.1e-4 of itself (a nineteenth of half a bf16 step), until it falls below
+// 2^-126 at x = 12.95, where the instruction flushes it to zero. An epilogue
+// thread runs 128 of these per 256 x 256 tile, of one special-function step each;
+// a slope takes a second one for exp(-x^2 / 2) (backward of 6432 x 1024 -> 4096:
+// 139.3 us; 137.7 with an exp(-x^2 / 2) times a polynomial that was off by a fifth of
+// itself at x = 5).
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -55,24 +61,23 @@ __device__ __forceinline__ float sigmoid_f(float z) {
   return FAST ? rcp_approx(1.f + exp2_approx(-kLog2e * z)) : 1.f / (1.f + expf(-z));
 }
 
-// x = min(|z|, 16), e = exp(-x^2 / 2); returns Phi(-x). At 16 the polynomial is still
-// finite and e is below the smallest normal number, which the instruction flushes to
-// zero: z e is zero for the largest finite z too. (The polynomial is no fit beyond 6,
-// where e < 2e-8 makes its error nothing.)
-constexpr float kPhiMax = 16.f;
+// x = min(|z|, 13.5); returns Phi(-x). At 13.5 it is zero (P < -136), so that z far
+// out gives z or 0 up to the largest finite values, and so is exp(-x^2 / 2).
+constexpr float kPhiMax = 13.5f;
+constexpr int kPhiDegree = 10;
 __device__ __forceinline__ float phi_poly(int k) {
-  constexpr float c[9] = {1.85581324e-5f,  -3.78031295e-4f, 3.25897020e-3f,
-                          -1.60708737e-2f, 5.25960136e-2f,  -1.27570483e-1f,
-                          2.48509570e-1f,  -3.98784939e-1f, 4.99997257e-1f};
+  constexpr float c[kPhiDegree + 1] = {
+      -3.65319136e-10f, 1.98518766e-08f,  -3.99899079e-07f, 2.70403029e-06f,
+      2.84406215e-05f,  -7.75194087e-04f, 8.07588827e-03f,  -5.33244498e-02f,
+      -4.58895057e-01f, -1.15114748e+00f, -9.99999106e-01f};
   return c[k];
 }
 __device__ __forceinline__ float phi_tail_fast(float z, float& x) {
   x = fminf(fabsf(z), kPhiMax);
-  const float e = exp2_approx(-0.5f * kLog2e * x * x);
   float q = phi_poly(0);
 #pragma unroll
-  for (int k = 1; k < 9; ++k) q = fmaf(q, x, phi_poly(k));
-  return q * e;
+  for (int k = 1; k <= kPhiDegree; ++k) q = fmaf(q, x, phi_poly(k));
+  return exp2_approx(q);
 }
 
 template <int ACT, bool FAST = false>
@@ -136,16 +141,14 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   return d;
 }
 
-// Phi(-|z|) of two values (phi_tail_fast): x = min(|z|, kPhiMax) and e = exp(-x^2 / 2)
-// too.
-__device__ __forceinline__ f32x2 phi_tail2(float z0, float z1, f32x2& x, f32x2& e) {
+// Phi(-|z|) of two values (phi_tail_fast), and x = min(|z|, kPhiMax).
+__device__ __forceinline__ f32x2 phi_tail2(float z0, float z1, f32x2& x) {
   x = pair(fminf(fabsf(z0), kPhiMax), fminf(fabsf(z1), kPhiMax));
-  const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
-  e = pair(exp2_approx(h.x), exp2_approx(h.y));
   f32x2 q = pair(phi_poly(0), phi_poly(0));
 #pragma unroll
-  for (int k = 1; k < 9; ++k) q = fma2(q, x, pair(phi_poly(k), phi_poly(k)));
-  return mul2(q, e);
+  for (int k = 1; k <= kPhiDegree; ++k) q = fma2(q, x, pair(phi_poly(k), phi_poly(k)));
+  const float2 h = halves(q);
+  return pair(exp2_approx(h.x), exp2_approx(h.y));
 }
 
 // act_f<ACT, true> of eight values; the GELU's polynomial two values at a time,
@@ -155,8 +158,8 @@ __device__ __forceinline__ void act8(float (&v)[8]) {
   if constexpr (ACT == DYRA_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      f32x2 x, e;
-      const f32x2 tail = phi_tail2(v[i], v[i + 1], x, e);
+      f32x2 x;
+      const f32x2 tail = phi_tail2(v[i], v[i + 1], x);
       const f32x2 minus = mul2(x, pair(-1.f, -1.f));
       const float2 y = halves(fma2(minus, tail, pair(v[i] < 0.f ? 0.f : v[i],
                                                      v[i + 1] < 0.f ? 0.f : v[i + 1])));
@@ -175,8 +178,10 @@ __device__ __forceinline__ void act_grad8(float (&v)[8]) {
   if constexpr (ACT == DYRA_ACT_GELU) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      f32x2 x, e;
-      const float2 tail = halves(phi_tail2(v[i], v[i + 1], x, e));
+      f32x2 x;
+      const float2 tail = halves(phi_tail2(v[i], v[i + 1], x));
+      const float2 h = halves(mul2(mul2(x, pair(-0.5f * kLog2e, -0.5f * kLog2e)), x));
+      const f32x2 e = pair(exp2_approx(h.x), exp2_approx(h.y));
       const f32x2 phi = pair(v[i] < 0.f ? tail.x : 1.f - tail.x,
                              v[i + 1] < 0.f ? tail.y : 1.f - tail.y);
       const float2 y = halves(fma2(mul2(pair(v[i], v[i + 1]), pair(kInvSqrt2Pi, kInvSqrt2Pi)), e,
