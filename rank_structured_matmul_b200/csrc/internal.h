@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <atomic>
 #include <cstdint>
+#include <mutex>
 
 namespace dyra {
 
@@ -16,7 +17,26 @@ constexpr int kMaxDevices = 64;
 struct KernelSetup {
   std::atomic<uint32_t> smem[kMaxDevices];  // dynamic shared memory configured so far
   std::atomic<int> occupancy[kMaxDevices];  // cached occupancy figure (e.g. resident pairs)
+  std::mutex mutex;                         // held while a limit is raised
 };
+
+// The dynamic shared memory limit of a kernel raised to `smem` bytes on device d (the
+// current one). One record per kernel, checked and set under its lock, so that no
+// host thread and no second caller ever lowers a limit that another relies on.
+template <class Kernel>
+inline int raise_smem(Kernel kfn, KernelSetup& setup, int d, uint32_t smem, bool carveout = true) {
+  if (d < 0 || d >= kMaxDevices) return -1;
+  if (smem <= setup.smem[d].load()) return 0;
+  std::lock_guard<std::mutex> lock(setup.mutex);
+  if (smem <= setup.smem[d].load()) return 0;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      (carveout && cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                        100) != cudaSuccess))
+    return -1;
+  setup.smem[d].store(smem);
+  return 0;
+}
 
 // The current device, or -1 if it cannot be read or is beyond kMaxDevices.
 inline int setup_device() {

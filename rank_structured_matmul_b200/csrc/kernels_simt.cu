@@ -986,12 +986,7 @@ int launch_solve(const float* TG, int splits, int64_t B, int k, int d_in, float 
   static KernelSetup setup;
   const int d = setup_device();
   if (d < 0) return -1;
-  if (smem > 48 * 1024 && smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return -1;
-    setup.smem[d].store(static_cast<uint32_t>(smem));
-  }
+  if (smem > 48 * 1024 && raise_smem(kfn, setup, d, static_cast<uint32_t>(smem), false)) return -1;
   cfg.gridDim = dim3(static_cast<unsigned>(B), static_cast<unsigned>((d_in + kSolveThreads - 1) / kSolveThreads));
   cfg.blockDim = dim3(kSolveThreads);
   cfg.dynamicSmemBytes = smem;
@@ -1103,12 +1098,7 @@ int launch_ltilde(const float* G, void* L, void* Llo, float* MD, int* flags, int
   static KernelSetup setup;
   const int d = setup_device();
   if (d < 0) return -1;
-  if (smem > 48 * 1024 && smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(ltilde_general_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return -1;
-    setup.smem[d].store(static_cast<uint32_t>(smem));
-  }
+  if (smem > 48 * 1024 && raise_smem(ltilde_general_kernel, setup, d, static_cast<uint32_t>(smem), false)) return -1;
   if ((T + kSolveThreads - 1) / kSolveThreads > 65535) return -1;
   cfg.gridDim = dim3(static_cast<unsigned>(B),
                      static_cast<unsigned>((T + kSolveThreads - 1) / kSolveThreads));
@@ -1135,12 +1125,7 @@ int launch_grid_transpose(const void* in, void* out, int64_t rows, int P, int Q,
   static KernelSetup setup;
   const int d = setup_device();
   if (d < 0) return -1;
-  if (smem > 48 * 1024 && smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(grid_transpose_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return -1;
-    setup.smem[d].store(static_cast<uint32_t>(smem));
-  }
+  if (smem > 48 * 1024 && raise_smem(grid_transpose_kernel, setup, d, static_cast<uint32_t>(smem), false)) return -1;
   const int64_t blocks = std::min<int64_t>(rows, static_cast<int64_t>(std::max(sm_count, 1)) * 8);
   grid_transpose_kernel<<<static_cast<unsigned>(blocks), kShuffleThreads, smem, s>>>(
       static_cast<const __nv_bfloat16*>(in), static_cast<__nv_bfloat16*>(out), rows, P, Q);

@@ -434,15 +434,8 @@ int launch_experts(const MoeShape& m, const float* In, const int* ids, const flo
                    int N, int* status, const DeviceInfo& dev, cudaStream_t s) {
   auto kfn = moe_tile_kernel<STAGE, VEC>;
   static KernelSetup setup;
-  const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
   constexpr uint32_t smem = kExRing * ExpertTile<STAGE>::Buf * 4;
-  if (smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return -1;
-    setup.smem[d].store(smem);
-  }
+  if (raise_smem(kfn, setup, dev.device, smem, false)) return -1;
   const int rows = STAGE == 0 ? m.f : m.d, steps = ((STAGE == 0 ? m.d : m.f) + kBk - 1) / kBk;
   const int tiles = (rows + kExRows - 1) / kExRows, reached = std::min(m.experts, N * m.top_k);
   // clusters while the blocks are fewer than two per SM and each keeps four steps
@@ -456,15 +449,8 @@ template <int BT, bool AMN, bool BMN, bool VEC>
 int launch_tile(const LinearGemm& g, int cs, const DeviceInfo& dev, cudaStream_t s) {
   auto kfn = linear_f32_kernel<BT, AMN, BMN, VEC>;
   static KernelSetup setup;
-  const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
   constexpr uint32_t smem = F32Tile<BT>::Floats * 4;
-  if (smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess)
-      return -1;
-    setup.smem[d].store(smem);
-  }
+  if (raise_smem(kfn, setup, dev.device, smem, false)) return -1;
   const int64_t mt = (g.M + BT - 1) / BT, jt = (g.J + BT - 1) / BT;
   if (mt * jt * cs > 0x7fffffffll) return -1;
   return launch_dependent(kfn, dim3(static_cast<unsigned>(mt * jt * cs)), dim3(256), smem, cs, s, g,

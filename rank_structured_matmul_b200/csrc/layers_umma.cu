@@ -501,9 +501,9 @@ int resident_clusters(int cs, const DeviceInfo& dev) {
   int n = known[dev.device][cs].load();
   if (n == 0) {
     n = split_resident<DenseSplitPolicy<false, false, true>>(cs, dev);
-    known[dev.device][cs].store(n);
+    known[dev.device][cs].store(n);  // (0: asked again)
   }
-  return n;
+  return n > 0 ? n : std::max(1, dev.sm_count / (2 * cs));
 }
 
 // CTA pairs or clusters, by a model of both in nanoseconds (plan_pairs; below), a

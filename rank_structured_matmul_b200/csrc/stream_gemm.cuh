@@ -533,39 +533,31 @@ uint32_t stream_setup(StreamCommon& c, int nb, bool a_mn, bool b_mn, float* ws, 
   return stream_smem_bytes(c.stages, c.b_bytes, Pol::kSmemBytes);
 }
 
-// Dynamic shared memory limits of the kernel raised to `smem` bytes.
-template <class Kernel>
-int raise_smem(Kernel kfn, KernelSetup& setup, uint32_t smem, const DeviceInfo& dev) {
-  const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
-  if (smem <= setup.smem[d].load()) return 0;
-  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess ||
-      cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-          cudaSuccess)
-    return -1;
-  setup.smem[d].store(smem);
-  return 0;
-}
-
 template <class Pol>
 int stream_launch(const typename Pol::Params& p, uint32_t smem, const DeviceInfo& dev,
                   cudaStream_t s) {
   auto kfn = stream_kernel<Pol>;
   static KernelSetup setup;
-  if (raise_smem(kfn, setup, smem, dev)) return -1;
+  if (raise_smem(kfn, setup, dev.device, smem)) return -1;
   return launch_dependent(kfn, dim3(static_cast<unsigned>(dev.sm_count)), dim3(kStreamThreads),
                           smem, 1, s, p);
 }
 
-// Clusters of cs CTAs that can be resident at once, at a CTA per SM.
+// split_kernel<Pol>'s record, of its launches and of the question below.
+template <class Pol>
+KernelSetup& split_setup() {
+  static KernelSetup setup;
+  return setup;
+}
+
+// Clusters of cs CTAs that can be resident at once, at a CTA per SM; 0 where that
+// cannot be told.
 template <class Pol>
 int split_resident(int cs, const DeviceInfo& dev) {
-  static KernelSetup setup;
   auto kfn = split_kernel<Pol>;
   const uint32_t smem = static_cast<uint32_t>(dev.max_smem_optin);
   int n = 0;
-  if (raise_smem(kfn, setup, smem, dev) == 0) {
+  if (raise_smem(kfn, split_setup<Pol>(), dev.device, smem) == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / cs * cs));
     cfg.blockDim = dim3(kStreamThreads);
@@ -580,15 +572,14 @@ int split_resident(int cs, const DeviceInfo& dev) {
     if (cudaOccupancyMaxActiveClusters(&n, kfn, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
-  return n > 0 ? n : std::max(1, dev.sm_count / (2 * cs));
+  return n;
 }
 
 template <class Pol>
 int split_launch(const typename Pol::Params& p, int tiles, int cs, uint32_t smem,
                  const DeviceInfo& dev, cudaStream_t s) {
   auto kfn = split_kernel<Pol>;
-  static KernelSetup setup;
-  if (raise_smem(kfn, setup, smem, dev)) return -1;
+  if (raise_smem(kfn, split_setup<Pol>(), dev.device, smem)) return -1;
   return launch_dependent(kfn, dim3(static_cast<unsigned>(tiles * cs)), dim3(kStreamThreads), smem,
                           cs, s, p, cs);
 }

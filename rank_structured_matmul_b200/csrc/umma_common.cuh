@@ -174,16 +174,7 @@ int launch_gemm(const typename Pol::Params& p, uint32_t smem, const DeviceInfo& 
   if (p.c.num_tiles <= 0) return 0;
   auto kfn = umma_gemm_kernel<Pol>;
   static KernelSetup setup;
-  const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
-  if (smem > setup.smem[d].load()) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-            cudaSuccess)
-      return -1;
-    setup.smem[d].store(smem);
-  }
+  if (raise_smem(kfn, setup, dev.device, smem)) return -1;
   cudaLaunchConfig_t cfg = {};
   // with clusters every CTA takes exactly one tile (the grid is the tile count)
   cfg.gridDim = dim3(static_cast<unsigned>(
@@ -218,17 +209,12 @@ int launch_gemm_pair(const typename Pol::Params& p, uint32_t smem, const DeviceI
   auto kfn = umma_gemm_pair_kernel<Pol>;
   static KernelSetup setup;  // occupancy: resident pairs at the configured size
   const int d = dev.device;
-  if (d < 0 || d >= kMaxDevices) return -1;
+  if (raise_smem(kfn, setup, d, smem)) return -1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(64 + 32 * EpiWarps<Pol>::value);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  if (smem > setup.smem[d].load() || setup.occupancy[d].load() < 1) {
-    if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(kfn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) !=
-            cudaSuccess)
-      return -1;
+  if (setup.occupancy[d].load() < 1) {  // (a CTA per SM at any of the sizes)
     cfg.gridDim = dim3(2 * (dev.sm_count / 2));
     int clusters = 0;
     if (cudaOccupancyMaxActiveClusters(&clusters, kfn, &cfg) != cudaSuccess || clusters < 1) {
@@ -236,7 +222,6 @@ int launch_gemm_pair(const typename Pol::Params& p, uint32_t smem, const DeviceI
       clusters = dev.sm_count / 2;
     }
     setup.occupancy[d].store(clusters);
-    if (smem > setup.smem[d].load()) setup.smem[d].store(smem);
   }
   const int max_pairs = setup.occupancy[d].load();
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(p.c.num_tiles, max_pairs)));
