@@ -124,8 +124,9 @@ int dyra_moe_create(dyra_moe_t *out, int d_model, int d_ff, int experts, int top
  *   Wr      : experts x d_model
  *   ids     : N x top_k int32 (output)
  *   weights : N x top_k float (output)
- * Logits are summed in fp64 from fp32 sums of eight products, so that experts
- * next to the border of the top_k are told apart as exactly as the inputs allow.
+ * Logits are summed in fp64, where the products of the inputs are exact: they are
+ * off by at most d_model 2^-53 of the sum of their products' magnitudes, and
+ * experts closer than that may come in either order.
  */
 int dyra_moe_route(dyra_moe_t p, const void *X, const void *Wr, int32_t *ids, float *weights,
                    int64_t N, dyra_stream_t stream);

@@ -193,10 +193,10 @@ int launch_act_backward_v(const T* dY, const T* Z, int act, T* dZ, T* dbias, int
 
 // ----------------------------------------------------------------- router ----
 // Logits of four experts x four tokens per block, its 256 threads sharing d in
-// pieces of eight: eight consecutive products are summed in fp32, then added in
-// fp64 (the choice of experts is discrete: logits next to the border of the top k
-// must not depend on the order of a long fp32 sum). The last block of a token
-// group to arrive then picks, a warp per token, the largest logit top_k times.
+// pieces of eight. The choice of experts is discrete, so the sums are fp64, in
+// which the products are exact: logits next to the border of the top k are told
+// apart down to d 2^-53 of their products' size. The last block of a token group
+// to arrive then picks, a warp per token, the largest logit top_k times.
 constexpr int kRouteTile = 4;
 
 template <typename T, bool VEC>
@@ -244,14 +244,17 @@ __global__ void __launch_bounds__(256)
       load8<T, VEC>(X + static_cast<size_t>(min(n0 + q, N - 1)) * m.d, i, m.d, x[q]);
     }
 #pragma unroll
-    for (int a = 0; a < R; ++a)
+    for (int j = 0; j < 8; ++j) {
+      double wd[R];
 #pragma unroll
-      for (int b = 0; b < R; ++b) {
-        float t = 0.f;
+      for (int b = 0; b < R; ++b) wd[b] = w[b][j];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t = fmaf(x[a][j], w[b][j], t);
-        acc[a][b] += t;
+      for (int a = 0; a < R; ++a) {
+        const double xd = x[a][j];
+#pragma unroll
+        for (int b = 0; b < R; ++b) acc[a][b] = fma(xd, wd[b], acc[a][b]);
       }
+    }
   }
   // the sixteen sums over the warp: at each step a lane keeps half of its values
   // and hands the other half to its partner, so lane l ends with value l / 2
