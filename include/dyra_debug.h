@@ -1,5 +1,5 @@
 /*
- * dyra_debug.h - diagnostics for include/dyra.h: read access to a plan's
+ * dyra_debug.h - diagnostics for include/dyra.h (and the layers of dyra_layers.h): read access to a plan's
  * intermediate buffers, so each stage of the forward can be checked on its own.
  * Not needed to run the layer.
  */
@@ -9,6 +9,7 @@
 #include <stddef.h>
 
 #include "dyra.h"
+#include "dyra_layers.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -64,6 +65,14 @@ int dyra_debug_set_stage_timing(dyra_plan_t p, int enable);
  * return DYRA_ERR_UNSUPPORTED. The output of a forward whose wait ran out is
  * not meaningful. */
 int dyra_debug_set_wait_limit(dyra_plan_t p, int stage, uint64_t ns);
+
+/* The same for a bf16 dense layer's or expert layer's calls from now on: the
+ * kernels on clusters (few rows) and of the experts, whose every CTA drains its own
+ * copies; those on CTA pairs keep the default. DYRA_ERR_UNSUPPORTED for handles on
+ * the CUDA cores, whose kernels have no such waits. After a wait that ran out,
+ * dyra_dense_status or dyra_moe_status makes the handle ready again. */
+int dyra_debug_dense_set_wait_limit(dyra_dense_t p, uint64_t ns);
+int dyra_debug_moe_set_wait_limit(dyra_moe_t p, uint64_t ns);
 
 /* Milliseconds of each of the 5 stages of the last forward (synchronises on
  * its final event). Returns DYRA_ERR_INVALID_ARG if timing was not enabled. */

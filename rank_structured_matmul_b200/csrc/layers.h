@@ -56,6 +56,8 @@ struct LinearGemm {
   int* status = nullptr;
   float* ws = nullptr;      // tensor cores: linear_ws_bytes of scratch
   int* counters = nullptr;  // tensor cores: linear_counters ints, zero between calls
+  // diagnostic limit of one pipeline wait of the clusters' kernel (0: the default)
+  unsigned long long wait_ns = 0;
 };
 
 // CUDA-core products: fp32 (layers_f32.cu), and bf16 for DYRA_KERNELS=simt
@@ -117,6 +119,7 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
                             const float* weights, const __nv_bfloat16* Wgu,
                             const __nv_bfloat16* Wd, const __nv_bfloat16* residual,
                             __nv_bfloat16* Y, int N, __nv_bfloat16* hidden, float* ws,
-                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s);
+                            int* counters, int* status, unsigned long long wait_ns,
+                            const DeviceInfo& dev, cudaStream_t s);
 
 }  // namespace dyra

@@ -11,6 +11,7 @@
 #include <new>
 
 #include "api_util.h"
+#include "dyra_debug.h"
 #include "layers.h"
 
 using namespace dyra;
@@ -28,6 +29,7 @@ struct dyra_dense {
   int* status = nullptr;
   void* base = nullptr;     // the one allocation that holds them
   size_t bytes = 0;
+  unsigned long long wait_ns = 0;  // diagnostic wait limit (0: the default)
 };
 
 struct dyra_moe {
@@ -43,6 +45,7 @@ struct dyra_moe {
   void* base = nullptr;    // the one allocation that holds them
   size_t bytes = 0;
   int n_tiles = 0;
+  unsigned long long wait_ns = 0;  // as above
 };
 
 namespace {
@@ -149,7 +152,7 @@ int moe_experts(const dyra_moe* p, const void* X, const int32_t* ids, const floa
                                      static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                      static_cast<const T*>(residual), static_cast<T*>(Y), n,
                                      static_cast<T*>(p->hidden), p->part,
-                                     p->tiles + moe_route_counters(), p->status, p->dev, s);
+                                     p->tiles + moe_route_counters(), p->status, p->wait_ns, p->dev, s);
   return launch_moe_experts_simt<T>(p->m, static_cast<const T*>(X), ids, weights,
                                     static_cast<const T*>(Wgu), static_cast<const T*>(Wd),
                                     static_cast<const T*>(residual), static_cast<T*>(Y), n,
@@ -279,6 +282,7 @@ int dyra_dense_forward(dyra_dense_t p, const void* X, const void* W, const void*
   g.status = p->status;
   g.ws = p->ws;
   g.counters = p->tiles;
+  g.wait_ns = p->wait_ns;
   return launched(linear(p, g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -322,6 +326,7 @@ int dyra_dense_backward(dyra_dense_t p, const void* dY, const void* X, const voi
   g.status = p->status;
   g.ws = p->ws;
   g.counters = p->tiles;
+  g.wait_ns = p->wait_ns;
   g.B = has_act ? dZ : dY;
   g.M = p->d_in;
   if (dX) {
@@ -357,6 +362,13 @@ int dyra_dense_destroy(dyra_dense_t p) {
   cudaDeviceSynchronize();
   dev_free(p->base);
   delete p;
+  return DYRA_OK;
+}
+
+int dyra_debug_dense_set_wait_limit(dyra_dense_t p, uint64_t ns) {
+  if (p == nullptr) return DYRA_ERR_INVALID_ARG;
+  if (p->simt) return DYRA_ERR_UNSUPPORTED;
+  p->wait_ns = ns;
   return DYRA_OK;
 }
 
@@ -461,6 +473,13 @@ int dyra_moe_destroy(dyra_moe_t p) {
   cudaDeviceSynchronize();
   dev_free(p->base);
   delete p;
+  return DYRA_OK;
+}
+
+int dyra_debug_moe_set_wait_limit(dyra_moe_t p, uint64_t ns) {
+  if (p == nullptr) return DYRA_ERR_INVALID_ARG;
+  if (p->simt) return DYRA_ERR_UNSUPPORTED;
+  p->wait_ns = ns;
   return DYRA_OK;
 }
 

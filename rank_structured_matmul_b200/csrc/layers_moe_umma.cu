@@ -378,7 +378,8 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
                             const float* weights, const __nv_bfloat16* Wgu,
                             const __nv_bfloat16* Wd, const __nv_bfloat16* residual,
                             __nv_bfloat16* Y, int N, __nv_bfloat16* hidden, float* ws,
-                            int* counters, int* status, const DeviceInfo& dev, cudaStream_t s) {
+                            int* counters, int* status, unsigned long long wait_ns,
+                            const DeviceInfo& dev, cudaStream_t s) {
   const int nb = ceil_div(N, 16) * 16;
   const int reached = std::min(m.experts, N * m.top_k);
   const MoeTables t{ids, weights, N, m.top_k, m.experts};
@@ -400,8 +401,10 @@ int launch_moe_experts_umma(const MoeShape& m, const __nv_bfloat16* X, const int
       !encode_3d(&w.tmW, Wd, m.f, m.d, m.experts, m.d, 128) ||
       !encode_3d(&w.tmH, hidden, m.f, N, reached, kMoeTokens, static_cast<uint32_t>(nb)))
     return -2;
-  const uint32_t smem_g = stream_setup<GateUpPolicy>(g.c, nb, false, false, ws, counters, status, dev);
-  const uint32_t smem_d = stream_setup<DownPolicy>(w.c, nb, false, false, ws, nullptr, status, dev);
+  const uint32_t smem_g =
+      stream_setup<GateUpPolicy>(g.c, nb, false, false, ws, counters, status, wait_ns, dev);
+  const uint32_t smem_d =
+      stream_setup<DownPolicy>(w.c, nb, false, false, ws, nullptr, status, wait_ns, dev);
   if (!smem_g || !smem_d) return -3;
   w.c.late_b = 1;
   if (stream_launch<GateUpPolicy>(g, smem_g, dev, s)) return -1;

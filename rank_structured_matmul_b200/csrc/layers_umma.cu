@@ -487,7 +487,7 @@ int launch_split(const LinearGemm& g, SplitChoice ch, const DeviceInfo& dev, cud
              : encode_2d(&p.tmB, g.B, g.K, g.J, static_cast<uint32_t>(ch.nb))))
     return -2;
   const uint32_t smem =
-      stream_setup<Pol>(p.c, ch.nb, kAMn, kBMn, nullptr, nullptr, g.status, dev);
+      stream_setup<Pol>(p.c, ch.nb, kAMn, kBMn, nullptr, nullptr, g.status, g.wait_ns, dev);
   if (!smem) return -3;
   return split_launch<Pol>(p, ceil_div(g.M, 128) * p.tiles_j, ch.cs, smem, dev, s);
 }

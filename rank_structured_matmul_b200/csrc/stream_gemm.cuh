@@ -55,7 +55,7 @@ struct StreamCommon {
   // 1: launched behind a grid that writes B, with everything else complete at
   // launch: A is copied before the dependency wait, B after it
   int late_b;
-  unsigned long long wait_ns;
+  unsigned long long wait_ns;  // limit of one pipeline wait; drains keep kWaitLimitNs
 };
 
 // A run of steps [k0, k0 + n) of run `sub` of `tile`.
@@ -139,18 +139,6 @@ __device__ __forceinline__ void stream_sum(const StreamCommon& c, int c0, int c1
     for (int i = 0; i < NV; ++i)
       if (i < n) v[i] += __ldcg(part + i * 128);
   }
-}
-
-// Barrier 1 over the epilogue's 128 threads; true if all of them say so.
-__device__ __forceinline__ bool stream_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, 1, 128, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
 }
 
 template <class Pol>
@@ -316,7 +304,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const int acc = local & 1;
       // all four warps go on or none: they meet at barriers in segment(), and
       // what the segment before left in shared memory has been read here
-      if (!stream_all(mbar_wait(tfull_bar(acc), (local >> 1) & 1, w))) break;
+      if (!all_threads(1, 128, mbar_wait(tfull_bar(acc), (local >> 1) & 1, w))) break;
       tc_fence_after();
       const uint32_t tacc = tmem + static_cast<uint32_t>(acc) * c.acc_cols +
                             (static_cast<uint32_t>(quad * 32) << 16);
@@ -442,7 +430,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
   } else {
     const int quad = warp & 3, row = quad * 32 + lane;
-    const bool good = stream_all(mbar_wait(done_bar, 0, w));
+    const bool good = all_threads(1, 128, mbar_wait(done_bar, 0, w));
     tc_fence_after();
     const int n = Pol::columns(p, tile);
     const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -514,7 +502,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 // of a block, or 0 if it does not fit.
 template <class Pol>
 uint32_t stream_setup(StreamCommon& c, int nb, bool a_mn, bool b_mn, float* ws, int* counters,
-                      int* status, const DeviceInfo& dev) {
+                      int* status, unsigned long long wait_ns, const DeviceInfo& dev) {
   c.nb = nb;
   c.b_bytes = static_cast<uint32_t>(nb) * 128u;
   c.acc_cols = static_cast<uint32_t>((nb + 31) / 32 * 32);
@@ -525,7 +513,7 @@ uint32_t stream_setup(StreamCommon& c, int nb, bool a_mn, bool b_mn, float* ws, 
   c.ws = ws;
   c.counters = counters;
   c.late_b = 0;
-  c.wait_ns = sm100::kWaitLimitNs;
+  c.wait_ns = wait_ns ? wait_ns : sm100::kWaitLimitNs;
   const int fixed = static_cast<int>(stream_smem_bytes(0, c.b_bytes, Pol::kSmemBytes));
   c.stages = std::min(kStreamMaxStages, (dev.max_smem_optin - fixed) /
                                             static_cast<int>(kStreamABytes + c.b_bytes));

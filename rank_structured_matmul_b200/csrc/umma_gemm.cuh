@@ -60,6 +60,9 @@ enum TraceSlot {
   kTrSplitReduced = 62   // split-K: this split's slice is reduced and stored
 };
 
+// Named barrier of the epilogue threads' vote to go on (the policies use 1 to 5).
+constexpr int kVoteBarrier = 6;
+
 struct GemmCommon {
   int num_tiles;
   int stages;
@@ -427,7 +430,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __maxnreg__(MaxRegs<Pol>::val
     for (int tile = blockIdx.x; tile < c.num_tiles; tile += gridDim.x, ++local) {
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      if (!mbar_wait(tfull_bar(acc), acc_phase, w)) break;
+      // all go on or none: they meet at barriers in the epilogue, and a thread
+      // whose wait ran out must not leave the others there
+      if (!all_threads(kVoteBarrier, 128, mbar_wait(tfull_bar(acc), acc_phase, w))) break;
       tc_fence_after();
       if (tr && e.tid == 0 && local == 0) tr[kTrEpiFirst] = globaltimer_ns();
       typename Pol::Tile t;

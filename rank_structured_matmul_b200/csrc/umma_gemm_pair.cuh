@@ -231,7 +231,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * EpiWarps<P
     for (int tile = pair; tile < c.num_tiles; tile += npairs, ++local) {
       const int acc = local & 1;
       const uint32_t acc_phase = (local >> 1) & 1;
-      if (!mbar_wait(tfull_bar(acc), acc_phase, w)) break;
+      // all of this CTA go on or none, as in the single-CTA skeleton
+      if (!all_threads(kVoteBarrier, 32 * EpiWarps<Pol>::value,
+                       mbar_wait(tfull_bar(acc), acc_phase, w)))
+        break;
       tc_fence_after();
       if (tr && e.tid == 0 && e.group == 0 && local == 0) tr[kTrEpiFirst] = globaltimer_ns();
       typename Pol::Tile t;

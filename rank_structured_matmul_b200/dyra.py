@@ -76,6 +76,8 @@ SIGNATURES = {
     "dyra_debug_stage_times": (_i, [_vp, ctypes.POINTER(ctypes.c_float)]),
     "dyra_debug_set_trace": (_i, [_vp, _i]),
     "dyra_debug_set_wait_limit": (_i, [_vp, _i, ctypes.c_uint64]),
+    "dyra_debug_dense_set_wait_limit": (_i, [_vp, ctypes.c_uint64]),
+    "dyra_debug_moe_set_wait_limit": (_i, [_vp, ctypes.c_uint64]),
     "dyra_debug_trace_bytes": (ctypes.c_size_t, []),
     "dyra_debug_trace_copy": (_i, [_vp, _vp, ctypes.c_size_t]),
 }

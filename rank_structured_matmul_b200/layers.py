@@ -97,6 +97,14 @@ def dyra_moe_destroy(p: int) -> None:
     _check(lib().dyra_moe_destroy(p), "dyra_moe_destroy")
 
 
+def dyra_debug_dense_set_wait_limit(p: int, ns: int) -> None:
+    _check(lib().dyra_debug_dense_set_wait_limit(p, ns), "dyra_debug_dense_set_wait_limit")
+
+
+def dyra_debug_moe_set_wait_limit(p: int, ns: int) -> None:
+    _check(lib().dyra_debug_moe_set_wait_limit(p, ns), "dyra_debug_moe_set_wait_limit")
+
+
 # ---- convenience objects ----
 
 def _activation(act: str) -> int:
