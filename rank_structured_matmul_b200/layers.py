@@ -8,7 +8,8 @@ libdyra.so's CUDA kernels and there is no fallback.
 Weights are arguments of each call. Tensors are contiguous CUDA tensors of the
 layer's type on the layer's device (the current device when it was made); a
 call runs on `stream` (default: that device's current stream), where its
-results are allocated too.
+results are allocated too. Torch records no gradient of these calls (the dense
+layer's are DenseLinear.backward's): where it would have to, the call is refused.
 """
 
 from __future__ import annotations
@@ -126,6 +127,7 @@ class _Layer:
         self.dtype = dtype
         self.torch_dtype = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
         self.int32, self.float32 = torch.int32, torch.float32
+        self._recording = torch.is_grad_enabled
         self.handle = None
         return DYRA_BF16 if dtype == "bf16" else DYRA_F32
 
@@ -142,6 +144,9 @@ class _Layer:
                 or t.get_device() != self.index or not t.is_contiguous():
             raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                              % (name, dtype or self.torch_dtype, tuple(shape), self.device))
+        if t.requires_grad and self._recording():  # the results would come without one
+            raise ValueError("%s requires a gradient, and torch records none of this call: make "
+                             "it under torch.no_grad() or with detached tensors" % name)
 
     def _rows(self, X, width, name="X"):
         if X is None or X.dim() != 2:
