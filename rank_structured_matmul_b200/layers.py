@@ -15,9 +15,10 @@ layer's are DenseLinear.backward's): where it would have to, the call is refused
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Optional
 
-from .dyra import DYRA_BF16, DYRA_F32, _check, _ptr, lib
+from .dyra import DYRA_BF16, DYRA_ERR_INVALID_ARG, DYRA_F32, DyraError, _check, _ptr, lib
 
 DYRA_ACT_NONE = 0
 DYRA_ACT_RELU = 1
@@ -33,7 +34,16 @@ DYRA_MOE_MAX_EXPERTS = 512
 
 # ---- raw C-ABI wrappers (same names; ints or tensors for pointers) ----
 
+def _c_ints(where: str, *values) -> None:
+    """Values that a C int does not hold are refused like other sizes out of range
+    (ctypes would pass their low 32 bits)."""
+    for v in values:
+        if not -2 ** 31 <= operator.index(v) < 2 ** 31:
+            raise DyraError(DYRA_ERR_INVALID_ARG, where)
+
+
 def dyra_dense_create(d_in: int, d_out: int, dtype: int) -> int:
+    _c_ints("dyra_dense_create", d_in, d_out, dtype)
     h = ctypes.c_void_p()
     _check(lib().dyra_dense_create(ctypes.byref(h), d_in, d_out, dtype), "dyra_dense_create")
     return h.value
@@ -64,6 +74,7 @@ def dyra_dense_destroy(p: int) -> None:
 
 def dyra_moe_create(d_model: int, d_ff: int, experts: int, top_k: int, act: int, renorm: int,
                     dtype: int) -> int:
+    _c_ints("dyra_moe_create", d_model, d_ff, experts, top_k, act, renorm, dtype)
     h = ctypes.c_void_p()
     _check(lib().dyra_moe_create(ctypes.byref(h), d_model, d_ff, experts, top_k, act, renorm,
                                  dtype), "dyra_moe_create")
