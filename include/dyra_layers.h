@@ -119,7 +119,7 @@ int dyra_moe_create(dyra_moe_t *out, int d_model, int d_ff, int experts, int top
 /*
  * The router: for each of N tokens the top_k experts by logit, largest first
  * (equal logits: the lower index first; a NaN counts as the lowest logit), and
- * their weights.
+ * their weights. A softmax that a NaN logit takes part in gives NaN weights.
  *   X       : N x d_model
  *   Wr      : experts x d_model
  *   ids     : N x top_k int32 (output)

@@ -17,6 +17,12 @@ namespace dyra {
 // wait is for the whole grid before, which waited for its own predecessor, so the
 // order of the stream holds. Calls that follow one another hide their launches
 // behind each other in this way.
+// One exception: the experts' down kernel (StreamCommon::late_b) reads the ids and
+// weights and copies Wd before its wait. It may, because the gate-up kernel, always
+// the one before it, lets it start only after its own wait is over: whatever wrote
+// those is complete then. Most other kernels here let the next one start at once, so
+// no other kernel may come between the two, and none may read before its wait
+// behind a grid that does so.
 template <class Kernel, class... Args>
 inline int launch_dependent(Kernel kfn, dim3 grid, dim3 block, uint32_t smem, int cluster,
                             cudaStream_t s, Args... args) {

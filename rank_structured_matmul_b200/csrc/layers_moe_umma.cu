@@ -139,6 +139,7 @@ struct GateUpPolicy {
           if (col + i >= p.t.N) break;
           const size_t at = (static_cast<size_t>(a) * kMoeTokens + col + i) * p.f + f;
           if (!in_bounds(p.c.status, at, 1, p.hidden_extent)) continue;
+          // rounded to bf16: an operand of the down product's tensor cores
           p.hidden[at] = __float2bfloat16_rn(act_f<decltype(tag)::value, true>(v[i]) *
                                              of(sm).up[col + i][row]);
         }

@@ -77,10 +77,10 @@ __global__ void __launch_bounds__(256) linear_simt_kernel(LinearGemm g, int64_t 
 // block of a column group to arrive adds the chunks in order and rounds once.
 // The pass is bound by the bytes it has in flight: four rows per thread, and as many
 // blocks as are resident at once: two per SM with Z, four without. 6432 x 4096 values
-// with the GELU take 32.8 us (4.8 TB/s; the ReLU 27.4, 5.8 TB/s), with four blocks per
-// SM 35.5, with three rows per thread 32.5 to 49.8 (GELU) and 42 (ReLU), with the
-// GELU's slope one value at a time 33.4; the column sums alone 12.4, with two blocks
-// per SM 14.6.
+// with the GELU take 35.3 us (4.5 TB/s; the ReLU 28.4, 5.6 TB/s), the column sums alone
+// 13.8. When this was chosen, with a GELU of 32.8: four blocks per SM 35.5, three rows
+// per thread 32.5 to 49.8 (GELU) and 42 (ReLU), the GELU's slope one value at a time
+// 33.4; the sums alone 12.4, with two blocks per SM 14.6.
 template <int ACT>
 constexpr int kActBlocks = ACT == DYRA_ACT_NONE ? 4 : 2;
 
@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(256, kActBlocks<ACT>)
           else if (ACT != DYRA_ACT_NONE)
             d *= slope[i];
           sum[i] += d;
+          // bf16: the tensor cores' operand of both products, rounded once (the sums
+          // are not); the gradients' error goes from 0.0017 to 0.0024
           out.v[i] = store_f<T>(d);
         }
         if (ACT != DYRA_ACT_NONE) *reinterpret_cast<P*>(dZ + at) = out;

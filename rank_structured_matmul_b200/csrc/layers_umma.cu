@@ -73,10 +73,12 @@ struct DensePairPolicy {
     int j0, m0, k0, nk;
     int tail, part;  // tail < 0: a whole tile; nk == 0: nothing
   };
-  // Four groups of four epilogue warps take the tile's 32-column store boxes in turn. A
-  // tile of K = 1024 takes 4.5 us of MMAs; its GELU, bias and stores took one group 13
-  // us, two groups 8, four 7 (ViT-L fc1 165, 49.3 and 47.0 us in all). A second box per
-  // group, for the residual on its way, pays for the operand stage it costs: 51 -> 48 us.
+  // Four groups of four epilogue warps take the tile's 32-column store boxes in turn.
+  // ViT-L fc1 (K = 1024, calls back to back on warm inputs) takes 81.0 us with one group,
+  // 55.8 with two, 46.7 with four; without bias and GELU 52.1, 41.2 and 39.5 (a bf16
+  // library product: 39.2), so that at this K the GELU's epilogue is still longer than
+  // a tile's MMAs. A second box per group, for the residual on its way, pays for the
+  // operand stage it costs: 51 -> 48 us.
   static constexpr int kEpiWarps = 16, kGroups = kEpiWarps / 4;
   static constexpr int kMaxRegs = 96;  // 576 threads
   static constexpr int kCols = 32;     // columns of a store box
@@ -509,7 +511,12 @@ int resident_clusters(int cs, const DeviceInfo& dev) {
 // CTA pairs or clusters, by a model of both in nanoseconds (plan_pairs; below), a
 // least-squares fit over the forward, dX and dW of nine shapes from 104 -> 96 to 4096
 // -> 14336 at 1 to 3000 rows with cold weights. Over those its choice is 1% slower
-// than the fastest on average, 15% at worst. 64 rows through 1024 -> 1024: 6.9 us in
+// than the fastest on average, 21% at worst (700 rows through 512 -> 2048, 13.1 us for
+// 10.8). Of choices that the model holds equal (under weights_ns, the weights' read)
+// the first, of fewest columns and CTAs, is taken: for one token through 4096 -> 14336
+// a CTA for each of the 112 tiles, 24.1 us; the fastest is 24.3. The pairs' side has
+// no such term: for sums far longer than those of the fit it may choose them wrongly.
+// 64 rows through 1024 -> 1024: 6.9 us in
 // clusters of 4, 15.3 on pairs; 450 rows through 4096 -> 14336: 56 on pairs, 105 in
 // clusters.
 SplitChoice choose_split(const LinearGemm& g, const DeviceInfo& dev) {

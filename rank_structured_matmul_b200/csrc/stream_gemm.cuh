@@ -3,9 +3,9 @@
 //
 // D tile = 128 rows of A (weights) x nb columns of B (tokens), accumulated over
 // steps of 64 k. All tiles' steps form one sequence, and the grid's CTAs take
-// equal contiguous shares of it (within one step), whatever the tile count: 112
-// tiles on 148 SMs keep every SM reading to the end, where a tile per CTA would
-// leave a quarter of them idle and two tiles on one in the next wave. A tile that
+// equal contiguous shares of it (within one step), whatever the tile count: the 32
+// down tiles of one token on two experts of 4096 x 14336 keep all 148 SMs reading to
+// the end, where a tile per CTA would leave most of them idle. A tile that
 // a share's border cuts is summed from the fp32 parts its CTAs leave in a
 // workspace, in the order of the CTAs, by the one that arrives last (or, where a
 // tile has many parts, by a grid that follows): no CTA waits for another, and the
@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // must stay behind the wait above: a late_b grid reads before its own
   if (!c.late_b) pdl_launch_dependents();
   const uint32_t tmem = words[0];
 

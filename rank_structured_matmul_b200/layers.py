@@ -16,7 +16,6 @@ from __future__ import annotations
 
 import ctypes
 import operator
-from typing import Optional
 
 from .dyra import DYRA_BF16, DYRA_ERR_INVALID_ARG, DYRA_F32, DyraError, _check, _ptr, lib
 
