@@ -91,7 +91,9 @@ int dyra_dense_backward(dyra_dense_t p, const void *dY, const void *X, const voi
                         int64_t N, dyra_stream_t stream);
 
 /* Synchronise the device, then return and clear the device status bits
- * (DYRA_STATUS_* of dyra.h), or a negative error code. */
+ * (DYRA_STATUS_* of dyra.h), or a negative error code. After a wait that ran out
+ * (DYRA_STATUS_WAIT_TIMEOUT) results mean nothing until this has been called: it
+ * makes the handle ready again. The same holds for dyra_moe_status. */
 int dyra_dense_status(dyra_dense_t p);
 size_t dyra_dense_device_bytes(dyra_dense_t p);
 /* Free the handle (synchronises the device). NULL is a no-op. */
